@@ -56,7 +56,8 @@ typedef enum {
 typedef enum {
     LI_DTYPE_F32 = 0,
     LI_DTYPE_BF16 = 1,
-    LI_DTYPE_E4M3 = 2 /* OCP FP8 e4m3 ("fn": no infinities, max 448) */
+    LI_DTYPE_E4M3 = 2, /* OCP FP8 e4m3 ("fn": no infinities, max 448) */
+    LI_DTYPE_E2M1 = 3  /* 4-bit cache rows (li_kv4_write) */
 } li_dtype;
 
 /* Longest score row li_topk accepts, and the largest k. */
@@ -451,6 +452,167 @@ size_t li_sparse_attention_workspace(int batch, int heads, int k);
 li_status li_sparse_attention(const void* q_bf16, const void* kv_bf16, int64_t cache_batch_rows, int64_t cache_rows,
                               const int32_t* sel, int batch, int heads, int k, float scale, float* out,
                               void* workspace, size_t workspace_bytes, li_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* A paged latent cache: block tables, positions, 4-bit rows                 */
+/* ------------------------------------------------------------------------ */
+/* Between a new token and its attention, a server that keeps its caches in
+ * pages decides where the token's row goes, rotates the positional part of its
+ * queries and row, and writes the row.  These calls do that on the device, so a
+ * decode step needs no host round trip and captures into a graph.
+ *
+ * A paged cache is `num_pages` pages of `page_size` rows, one after another.  Its
+ * slot p * page_size + i is row i of page p.  Request r's position s lies in page
+ * block_table[r * max_blocks + s / page_size], at row s % page_size. */
+
+/* Most requests li_block_tables takes. */
+#define LI_BLOCK_TABLE_MAX_REQUESTS 16384
+
+/* Block tables and slot maps of one step, from the requests' lengths.  Request r
+ * has seq_lens[r] positions after the step, the last new_lens[r] of them new.  It
+ * already holds the ceil((seq - new) / page_size) first entries of its table row;
+ * the ones up to ceil(seq / page_size) are taken from free_pages, in request
+ * order, starting at entry *free_start (NULL: 0).
+ *   seq_lens, new_lens  [requests] int32
+ *   block_table  [requests, max_blocks] int32 (in/out; entries past a request's
+ *                length are left as they were)
+ *   free_pages   [n_free] int32     free_start  [1] int32, or NULL
+ * New tokens are numbered request by request (a request's tokens in order):
+ *   slots      [max_tokens] int64 (out): cache slot of each new token, -1 = none
+ *   positions  [max_tokens] int32 (out): its position in the request
+ *   requests_of [max_tokens] int32 (out): its request
+ *   starts     [requests + 1] int32 (out): first token of each request, then the total
+ *   free_next  [1] int32 (out): the first entry of free_pages not taken; may not
+ *              be free_start itself (pass the two buffers in turn)
+ * Entries of the three token arrays after the last token are -1, which the calls
+ * below take as padding.  Reported as LI_ERR_BOUNDS by li_get_last_error:
+ *   - new < 0, new > seq or seq > max_blocks * page_size: the request counts as
+ *     having no new token and takes no page;
+ *   - more pages needed than free ones, or a page outside [0, num_pages): that
+ *     table entry becomes -1 (a held entry is left), the slots in it -1;
+ *   - more new tokens than max_tokens: the ones that do not fit are not listed. */
+li_status li_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int requests, int32_t* block_table,
+                          int max_blocks, int page_size, int num_pages, const int32_t* free_pages, int n_free,
+                          const int32_t* free_start, int max_tokens, int64_t* slots, int32_t* positions,
+                          int32_t* requests_of, int32_t* starts, int32_t* free_next, li_stream_t stream);
+
+/* Rotary frequencies.  Pair i of rot_dim / 2 turns by f_i radians a position,
+ * f_i = base^(-2 i / rot_dim), scaled for long contexts:
+ *   LI_ROPE_PLAIN   f_i
+ *   LI_ROPE_LINEAR  f_i / factor
+ *   LI_ROPE_YARN    f_i / factor for pairs that make fewer than beta_slow turns over
+ *                   original_len positions, f_i for those that make more than
+ *                   beta_fast, a linear ramp over the pairs in between (its ends
+ *                   rounded outward to whole pairs, as YaRN defines them)
+ * turns (HOST memory, [rot_dim / 2]): f_i / (2 pi) turns, modulo 1, as 64-bit
+ * fixed-point fractions.  The caller uploads them once.  rot_dim even, 2..1024;
+ * base > 1; factor >= 1; original_len >= 1 and beta_fast > beta_slow > 0 (YaRN). */
+typedef enum { LI_ROPE_PLAIN = 0, LI_ROPE_LINEAR = 1, LI_ROPE_YARN = 2 } li_rope_scaling;
+li_status li_rope_table(int rot_dim, double base, int scaling, double factor, int original_len, double beta_fast,
+                        double beta_slow, uint64_t* turns);
+
+typedef enum { LI_ROPE_INTERLEAVED = 0, LI_ROPE_HALF = 1 } li_rope_layout;
+typedef struct {
+    const void* x;            /* [tokens, heads, dim], elements of a head next to each other */
+    void* out;                /* same shape; may be x itself with x's strides */
+    int64_t x_token_stride;   /* elements */
+    int64_t x_head_stride;
+    int64_t out_token_stride;
+    int64_t out_head_stride;
+    int heads;
+    int dim;
+    int offset;               /* the rotated part is [offset, offset + rot_dim) of a head */
+    int layout;               /* li_rope_layout: pairs (2i, 2i + 1), or (i, i + rot_dim / 2) */
+    li_dtype dtype;           /* LI_DTYPE_BF16 or LI_DTYPE_F32 */
+} li_rope_tensor;
+
+/* Most tensors of one li_rope call. */
+#define LI_ROPE_MAX_TENSORS 4
+
+/* Rotates up to four tensors of the same tokens (queries and keys, of the indexer
+ * and of the attention) in one launch:
+ *     (a, b) -> mscale * (a cos - b sin, a sin + b cos),  angle = position * f_i.
+ * The rest of a head is copied, or left alone when out is x.  The angle is reduced
+ * exactly; the rotation is computed in fp32 and rounded once.  A token whose position
+ * is negative is padding: its row of out is left as it was.
+ *   positions [tokens] int32      turns [rot_dim / 2] uint64 (device; li_rope_table)
+ * Any strides and alignment (16-byte items where every one allows it); x and out are
+ * the same tensor or do not overlap, and the tensors of a call do not overlap. */
+li_status li_rope(const li_rope_tensor* tensors, int n_tensors, int tokens, const int32_t* positions,
+                  const uint64_t* turns, int rot_dim, float mscale, li_stream_t stream);
+
+/* Bytes of a 4-bit cache row. */
+#define LI_KV4_ROW_BYTES 416
+
+/* The 4-bit form of the consumer's 576-element row (512 latent + 64 rotary): 256
+ * bytes of e2m1 codes (element 2i in the low half of byte i, 2i + 1 in the high
+ * half; magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6, sign in the top bit), 32 e4m3 scales
+ * (one per 16 elements), 64 rotary elements as they are in bf16.  Per block of 16:
+ *     s = e4m3(min(absmax / 6, 448)),   code_i = e2m1(x_i / s)   (nearest, ties to even;
+ * beyond 6 the largest code; all zero when s is zero).  The value held is code * s,
+ * which bf16 holds exactly.  A block with a NaN gets a NaN scale: it reads as NaN.
+ *   rows   [n, 576] bf16, `row_stride` elements apart (>= 576)
+ *   slots  [n] int64 (li_block_tables); < 0 is skipped, one outside the cache is
+ *          skipped and reported as LI_ERR_BOUNDS.  Slots of a call must differ: of two
+ *          rows sent to the same slot either may remain, or parts of both.
+ *   cache  [num_slots] rows of LI_KV4_ROW_BYTES, 16-byte aligned */
+li_status li_kv4_write(const void* rows_bf16, int64_t row_stride, const int64_t* slots, int64_t n, void* cache,
+                       int64_t num_slots, li_stream_t stream);
+/* The rows at `slots` as bf16: out [n, 576], 16-byte aligned.  A slot < 0 reads as
+ * zeros, one outside the cache too, and is reported as LI_ERR_BOUNDS. */
+li_status li_kv4_read(const void* cache, int64_t num_slots, const int64_t* slots, int64_t n, void* out_bf16,
+                      li_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention over a paged latent cache                                       */
+/* ------------------------------------------------------------------------ */
+typedef struct {
+    int rows;          /* query tokens */
+    int heads;         /* any number >= 1 (whole groups of 64 waste nothing) */
+    int requests;      /* rows of block_table */
+    int num_pages;     /* of the cache */
+    int page_size;     /* rows of a page, any number >= 1 */
+    int max_blocks;    /* entries of a request's block_table row */
+    li_dtype cache_dtype; /* LI_DTYPE_E2M1: rows of LI_KV4_ROW_BYTES; LI_DTYPE_BF16: rows of 576 bf16 */
+    float scale;       /* softmax scale, finite and > 0 */
+} li_attn_desc;
+
+/* The consumer's attention (li_sparse_attention's definition) over a paged cache,
+ * in 4 bits or bf16, for any head count, with several query tokens per request:
+ *     out[t,h,:] = sum_i p_i * c[sel[t,i], 0:512],
+ *     p = softmax over the valid i of scale * (q[t,h,:] . c[sel[t,i], :])
+ *   q_bf16       [rows, heads, 576] bf16, 16-byte aligned
+ *   cache        num_pages * page_size rows, 16-byte aligned
+ *   block_table  [requests, max_blocks] int32, or NULL: page r * max_blocks + b
+ *                (a dense cache [requests, L] is page_size = L, max_blocks = 1)
+ *   requests_of  [rows] int32: each token's request, or NULL: token t is request t's.
+ *                A negative one is padding: the token's row of out is left as it was.
+ *   sel          [rows, k] int32 positions in the token's request (li_topk's output, any
+ *                order; -1 = none; one listed twice counts twice)
+ *   out_bf16     [rows, heads, 512] bf16, 16-byte aligned.  The softmax weights are
+ *                rounded to bf16 for the value product, sums and statistics are fp32.
+ *   workspace    li_paged_attention_workspace(rows, heads, k) bytes, 256-byte aligned
+ *                (may be 0: then NULL).  Calls that overlap in time must not share one.
+ * A token with no valid selection gets 0.  Selections outside [0, max_blocks *
+ * page_size) or in a page outside the cache are skipped and reported as
+ * LI_ERR_BOUNDS by li_get_last_error; a request outside [0, requests) is reported and
+ * its token treated as padding.  Positions nothing selects are never read. */
+li_status li_paged_sparse_attention(const void* q_bf16, const void* cache, const int32_t* block_table,
+                                    const int32_t* requests_of, const int32_t* sel, int k, const li_attn_desc* desc,
+                                    void* out_bf16, void* workspace, size_t workspace_bytes, li_stream_t stream);
+
+/* The same attention over a sliding window and the first `sinks` positions: the token
+ * at position p of its request sees the positions s <= p with s < sinks or
+ * s > p - window.  window >= max_len is plain causal attention.
+ *   positions  [rows] int32: each token's position (li_block_tables); a negative one is
+ *              padding, one >= max_len is reported as LI_ERR_BOUNDS and treated as padding
+ *   window >= 1, sinks >= 0, 1 <= max_len <= max_blocks * page_size
+ *   workspace  li_paged_attention_workspace(rows, heads, min(max_len, window + sinks)) bytes */
+li_status li_window_attention(const void* q_bf16, const void* cache, const int32_t* block_table,
+                              const int32_t* requests_of, const int32_t* positions, int window, int sinks, int max_len,
+                              const li_attn_desc* desc, void* out_bf16, void* workspace, size_t workspace_bytes,
+                              li_stream_t stream);
+size_t li_paged_attention_workspace(int rows, int heads, int positions);
 
 /* ------------------------------------------------------------------------ */
 /* Graphs whose kernels keep their streams' priorities                       */

@@ -12,10 +12,15 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libli.so")
 
 LI_OK, LI_ERR_INVALID_ARG, LI_ERR_UNSUPPORTED, LI_ERR_CUDA, LI_ERR_TIMEOUT, LI_ERR_BOUNDS = range(6)
-LI_DTYPE_F32, LI_DTYPE_BF16, LI_DTYPE_E4M3 = 0, 1, 2
+LI_DTYPE_F32, LI_DTYPE_BF16, LI_DTYPE_E4M3, LI_DTYPE_E2M1 = 0, 1, 2, 3
 LI_TOPK_MAX_LEN = 262144
 LI_HS_NOALLOC_MAX_SCRATCH_FLOATS = 1048576
 LI_OP_SCORE, LI_OP_TOPK, LI_OP_HS, LI_OP_DECODE_SELECT = range(4)
+LI_BLOCK_TABLE_MAX_REQUESTS = 16384
+LI_KV4_ROW_BYTES = 416
+LI_ROPE_PLAIN, LI_ROPE_LINEAR, LI_ROPE_YARN = range(3)
+LI_ROPE_INTERLEAVED, LI_ROPE_HALF = range(2)
+LI_ROPE_MAX_TENSORS = 4
 
 vp = ctypes.c_void_p
 i32 = ctypes.c_int
@@ -26,6 +31,17 @@ sz = ctypes.c_size_t
 class ScoreDesc(ctypes.Structure):
     _fields_ = [("rows", i32), ("heads", i32), ("dim", i32), ("max_len", i32), ("causal", i32),
                 ("causal_offset", i32), ("q_dtype", i32), ("k_dtype", i32), ("tokens_per_request", i32)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("rows", i32), ("heads", i32), ("requests", i32), ("num_pages", i32), ("page_size", i32),
+                ("max_blocks", i32), ("cache_dtype", i32), ("scale", ctypes.c_float)]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", vp), ("out", vp), ("x_token_stride", i64), ("x_head_stride", i64), ("out_token_stride", i64),
+                ("out_head_stride", i64), ("heads", i32), ("dim", i32), ("offset", i32), ("layout", i32),
+                ("dtype", i32)]
 
 
 # name -> (restype, argtypes); every symbol declared in include/li.h
@@ -59,6 +75,14 @@ SIGNATURES = {
     "li_hs_refine_fp8": (i32, [vp, vp, i64, i64, vp, i32, i32, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]),
     "li_sparse_attention": (i32, [vp, vp, i64, i64, vp, i32, i32, i32, ctypes.c_float, vp, vp, sz, vp]),
     "li_sparse_attention_workspace": (sz, [i32, i32, i32]),
+    "li_block_tables": (i32, [vp, vp, i32, vp, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp]),
+    "li_rope_table": (i32, [i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double, vp]),
+    "li_rope": (i32, [ctypes.POINTER(RopeTensor), i32, i32, vp, vp, i32, ctypes.c_float, vp]),
+    "li_kv4_write": (i32, [vp, i64, vp, i64, vp, i64, vp]),
+    "li_kv4_read": (i32, [vp, i64, vp, i64, vp, vp]),
+    "li_paged_sparse_attention": (i32, [vp, vp, vp, vp, vp, i32, ctypes.POINTER(AttnDesc), vp, vp, sz, vp]),
+    "li_window_attention": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, ctypes.POINTER(AttnDesc), vp, vp, sz, vp]),
+    "li_paged_attention_workspace": (sz, [i32, i32, i32]),
     "li_graph_instantiate": (i32, [vp, i32, ctypes.POINTER(ctypes.c_void_p)]),
     "li_graph_launch": (i32, [vp, vp]),
     "li_graph_destroy": (i32, [vp]),

@@ -4,6 +4,7 @@
 // (except li_get_last_error).
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "li_common.cuh"
@@ -50,6 +51,20 @@ bool encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uin
     cuuint32_t estr[2] = {1, 1};
     return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D tensor map over [planes, rows, row_elems] dense bf16, box [64, box_rows, 1], 128-byte swizzle.
+bool encode_map_3d_bf16(CUtensorMap* m, const void* base, uint64_t row_elems, uint64_t rows, uint64_t planes,
+                        uint32_t box_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {row_elems, rows, planes};
+    cuuint64_t strides[2] = {row_elems * 2, row_elems * 2 * rows};
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -677,6 +692,234 @@ li_status li_sparse_attention(const void* q_bf16, const void* kv_bf16, int64_t c
     a.out = out;
     a.err = e;
     return launch_sparse_attn(qmap, a, stream);
+}
+
+li_status li_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int requests, int32_t* block_table,
+                          int max_blocks, int page_size, int num_pages, const int32_t* free_pages, int n_free,
+                          const int32_t* free_start, int max_tokens, int64_t* slots, int32_t* positions,
+                          int32_t* requests_of, int32_t* starts, int32_t* free_next, li_stream_t stream) {
+    if (requests < 0 || max_blocks < 0 || page_size < 1 || num_pages < 0 || n_free < 0 || max_tokens < 0)
+        return LI_ERR_INVALID_ARG;
+    if (requests > LI_BLOCK_TABLE_MAX_REQUESTS) return LI_ERR_UNSUPPORTED;
+    if (requests > 0 && (!seq_lens || !new_lens || (max_blocks > 0 && !block_table))) return LI_ERR_INVALID_ARG;
+    if (max_tokens > 0 && (!slots || !positions || !requests_of)) return LI_ERR_INVALID_ARG;
+    if (!starts || !free_next || free_next == free_start || (n_free > 0 && !free_pages)) return LI_ERR_INVALID_ARG;
+    if (!aligned(slots, 8) || !aligned(positions, 4) || !aligned(requests_of, 4) || !aligned(starts, 4) ||
+        !aligned(free_next, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) ||
+        !aligned(free_pages, 4) || !aligned(free_start, 4))
+        return LI_ERR_INVALID_ARG;
+    BlockTableArgs a{seq_lens, new_lens, block_table, free_pages, free_start, requests, max_blocks, page_size,
+                     num_pages, n_free, max_tokens, slots, positions, requests_of, starts, free_next, {}};
+    if (ready(&a.err) != LI_OK) return LI_ERR_CUDA;
+    return launch_block_tables(a, stream);
+}
+
+li_status li_rope_table(int rot_dim, double base, int scaling, double factor, int original_len, double beta_fast,
+                        double beta_slow, uint64_t* turns) {
+    if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0 || !turns) return LI_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !(base < 1e30)) return LI_ERR_INVALID_ARG;
+    if (scaling != LI_ROPE_PLAIN && scaling != LI_ROPE_LINEAR && scaling != LI_ROPE_YARN) return LI_ERR_INVALID_ARG;
+    if (scaling != LI_ROPE_PLAIN && (!(factor >= 1.0) || !(factor < 1e30))) return LI_ERR_INVALID_ARG;
+    if (scaling == LI_ROPE_YARN &&
+        (original_len < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !(beta_fast < 1e30)))
+        return LI_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586476925286766559;
+    double lo = 0.0, hi = 0.0;
+    if (scaling == LI_ROPE_YARN) {
+        // the (fractional) pair that makes beta turns over original_len positions
+        auto pair_of = [&](double beta) {
+            return rot_dim * std::log(original_len / (beta * two_pi)) / (2.0 * std::log(base));
+        };
+        lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+        hi = std::fmin(std::ceil(pair_of(beta_slow)), rot_dim - 1.0);
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == LI_ROPE_LINEAR) f /= factor;
+        if (scaling == LI_ROPE_YARN) {
+            const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        turns[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 64));  // f <= 1: below 2^62
+    }
+    return LI_OK;
+}
+
+li_status li_rope(const li_rope_tensor* tensors, int n_tensors, int tokens, const int32_t* positions,
+                  const uint64_t* turns, int rot_dim, float mscale, li_stream_t stream) {
+    if (!tensors || n_tensors < 1 || n_tensors > LI_ROPE_MAX_TENSORS || tokens < 0) return LI_ERR_INVALID_ARG;
+    if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0) return LI_ERR_INVALID_ARG;
+    if (!(mscale > -3.0e38f) || !(mscale < 3.0e38f)) return LI_ERR_INVALID_ARG;
+    RopeArgs a{};
+    a.n = n_tensors;
+    a.tokens = tokens;
+    a.rot_dim = rot_dim;
+    a.positions = positions;
+    a.turns = turns;
+    a.mscale = mscale;
+    a.wide = 1;
+    long long items = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        const li_rope_tensor& s = tensors[i];
+        if (s.dtype != LI_DTYPE_BF16 && s.dtype != LI_DTYPE_F32) return LI_ERR_UNSUPPORTED;
+        if (s.layout != LI_ROPE_INTERLEAVED && s.layout != LI_ROPE_HALF) return LI_ERR_INVALID_ARG;
+        if (s.heads < 1 || s.dim < rot_dim || s.offset < 0 || s.offset > s.dim - rot_dim) return LI_ERR_INVALID_ARG;
+        if (s.x_token_stride < 0 || s.x_head_stride < 0 || s.out_token_stride < 0 || s.out_head_stride < 0)
+            return LI_ERR_INVALID_ARG;
+        const bool bf16 = s.dtype == LI_DTYPE_BF16;
+        const int v = bf16 ? 8 : 4, size = bf16 ? 2 : 4;
+        if (tokens > 0 && (!s.x || !s.out || !aligned(s.x, size) || !aligned(s.out, size))) return LI_ERR_INVALID_ARG;
+        const bool in_place = s.x == s.out;
+        if (in_place && ((s.x_token_stride != s.out_token_stride && tokens > 1) ||
+                         (s.x_head_stride != s.out_head_stride && s.heads > 1)))
+            return LI_ERR_INVALID_ARG;
+        // a row of out that holds another's elements would be written twice
+        const int64_t span = s.heads > 1 ? (s.heads - 1) * s.out_head_stride + s.dim : s.dim;
+        if (s.heads > 1 && s.out_head_stride < s.dim && !(tokens > 0 && s.out_token_stride >= s.dim &&
+            s.out_head_stride >= (tokens - 1) * s.out_token_stride + s.dim))
+            return LI_ERR_INVALID_ARG;
+        if (tokens > 1 && s.out_token_stride < span && !(s.out_token_stride >= s.dim && s.heads > 1 &&
+            s.out_head_stride >= (tokens - 1) * s.out_token_stride + s.dim))
+            return LI_ERR_INVALID_ARG;
+        if (!aligned(s.x, 16) || !aligned(s.out, 16) || s.offset % v != 0 || s.dim % v != 0 ||
+            rot_dim % (s.layout == LI_ROPE_HALF ? 2 * v : v) != 0 ||
+            (s.x_token_stride | s.x_head_stride | s.out_token_stride | s.out_head_stride) % v != 0)
+            a.wide = 0;
+        items += (long long)s.heads * s.dim;
+        a.t[i] = RopeTensor{s.x, s.out, s.x_token_stride, s.x_head_stride, s.out_token_stride, s.out_head_stride,
+                            s.heads, s.offset, s.dim, s.layout == LI_ROPE_HALF, bf16, in_place, 0, 0};
+    }
+    if (items >= (1ll << 30)) return LI_ERR_UNSUPPORTED;
+    if (tokens == 0) return LI_OK;
+    if (!positions || !turns || !aligned(positions, 4) || !aligned(turns, 8)) return LI_ERR_INVALID_ARG;
+    // memory written by one tensor of the call is neither read nor written through another
+    for (int i = 0; i < n_tensors; ++i) {
+        const auto range = [&](const void* p, int64_t ts, int64_t hs, const RopeTensor& t) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            return std::pair<uintptr_t, uintptr_t>(
+                at, at + ((tokens - 1) * ts + (t.heads - 1) * hs + t.dim) * (t.bf16 ? 2 : 4));
+        };
+        const RopeTensor& t = a.t[i];
+        const auto o = range(t.out, t.out_token, t.out_head, t);
+        for (int j = 0; j < n_tensors; ++j) {
+            const RopeTensor& s = a.t[j];
+            const auto x = range(s.x, s.x_token, s.x_head, s), y = range(s.out, s.out_token, s.out_head, s);
+            const bool same = i == j;
+            // views of one buffer (the heads of a fused projection) interleave without sharing an element:
+            // they are recognised by their common token stride and separate spans within a token
+            const auto apart = [&](const std::pair<uintptr_t, uintptr_t>& r, int64_t ts, int64_t hs) {
+                if (r.second <= o.first || o.second <= r.first) return true;
+                const int size = t.bf16 ? 2 : 4, other = s.bf16 ? 2 : 4;
+                if (ts * other != t.out_token * size || ts == 0) return false;
+                const uintptr_t w = (uintptr_t)ts * other;
+                const uintptr_t rs = ((s.heads - 1) * hs + s.dim) * (uintptr_t)other;
+                const uintptr_t os = ((t.heads - 1) * t.out_head + t.dim) * (uintptr_t)size;
+                const uintptr_t d = r.first >= o.first ? (r.first - o.first) % w : (w - (o.first - r.first) % w) % w;
+                return d >= os && d + rs <= w;
+            };
+            if (!(same && t.in_place) && !apart(x, s.x_token, s.x_head)) return LI_ERR_INVALID_ARG;
+            if (!same && !apart(y, s.out_token, s.out_head)) return LI_ERR_INVALID_ARG;
+        }
+    }
+    DevErr e;
+    if (ready(&e) != LI_OK) return LI_ERR_CUDA;
+    return launch_rope(a, stream);
+}
+
+li_status li_kv4_write(const void* rows_bf16, int64_t row_stride, const int64_t* slots, int64_t n, void* cache,
+                       int64_t num_slots, li_stream_t stream) {
+    if (n < 0 || num_slots < 0 || row_stride < 576) return LI_ERR_INVALID_ARG;
+    if (n >= (1ll << 31) || num_slots >= (1ll << 50)) return LI_ERR_UNSUPPORTED;
+    if (n == 0) return LI_OK;
+    if (!rows_bf16 || !slots || !cache || !aligned(rows_bf16, 2) || !aligned(slots, 8) || !aligned(cache, 16))
+        return LI_ERR_INVALID_ARG;
+    Kv4Args a{static_cast<const uint16_t*>(rows_bf16), nullptr, static_cast<uint8_t*>(cache), slots, n, num_slots,
+              row_stride, aligned(rows_bf16, 16) && row_stride % 8 == 0, {}};
+    if (ready(&a.err) != LI_OK) return LI_ERR_CUDA;
+    return launch_kv4_write(a, stream);
+}
+
+li_status li_kv4_read(const void* cache, int64_t num_slots, const int64_t* slots, int64_t n, void* out_bf16,
+                      li_stream_t stream) {
+    if (n < 0 || num_slots < 0) return LI_ERR_INVALID_ARG;
+    if (n >= (1ll << 31) || num_slots >= (1ll << 50)) return LI_ERR_UNSUPPORTED;
+    if (n == 0) return LI_OK;
+    if (!cache || !slots || !out_bf16 || !aligned(cache, 16) || !aligned(slots, 8) || !aligned(out_bf16, 16))
+        return LI_ERR_INVALID_ARG;
+    Kv4Args a{nullptr, static_cast<uint16_t*>(out_bf16), static_cast<uint8_t*>(const_cast<void*>(cache)), slots, n,
+              num_slots, 0, 1, {}};
+    if (ready(&a.err) != LI_OK) return LI_ERR_CUDA;
+    return launch_kv4_read(a, stream);
+}
+
+size_t li_paged_attention_workspace(int rows, int heads, int positions) {
+    if (rows <= 0 || heads <= 0 || positions <= 0) return 0;
+    return paged_attn_workspace_bytes(rows, heads, paged_attn_splits(rows, heads, positions, host_num_sms()));
+}
+
+// The two forms' common checks and launch; `positions` is the longest visible list.
+static li_status paged_attention(const void* q, PagedAttnArgs a, const li_attn_desc& d, int positions, void* out,
+                                 void* workspace, size_t workspace_bytes, li_stream_t stream) {
+    if (d.rows < 0 || d.heads < 1 || d.requests < 0 || d.num_pages < 0 || d.page_size < 1 || d.max_blocks < 0)
+        return LI_ERR_INVALID_ARG;
+    if (!(d.scale > 0.f) || !(d.scale < 3.0e38f)) return LI_ERR_INVALID_ARG;
+    if (d.cache_dtype != LI_DTYPE_E2M1 && d.cache_dtype != LI_DTYPE_BF16) return LI_ERR_UNSUPPORTED;
+    if (d.heads > 4096 || positions > (1 << 28)) return LI_ERR_UNSUPPORTED;
+    if (d.rows == 0) return LI_OK;
+    if (!a.req && d.rows > d.requests) return LI_ERR_INVALID_ARG;
+    if (!a.table && (int64_t)d.requests * d.max_blocks > d.num_pages) return LI_ERR_INVALID_ARG;
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return LI_ERR_INVALID_ARG;
+    if ((!a.cache && d.num_pages > 0) || !aligned(a.cache, 16)) return LI_ERR_INVALID_ARG;
+    a.rows = d.rows;
+    a.heads = d.heads;
+    a.requests = d.requests;
+    a.num_pages = d.num_pages;
+    a.page_size = d.page_size;
+    a.max_blocks = d.max_blocks;
+    a.scale = d.scale;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.hgroups = (d.heads + 63) / 64;
+    const size_t need = li_paged_attention_workspace(d.rows, d.heads, positions);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return LI_ERR_INVALID_ARG;
+    if (ready(&a.err) != LI_OK) return LI_ERR_CUDA;
+    a.splits = positions > 0 ? paged_attn_splits(d.rows, d.heads, positions, host_num_sms()) : 1;
+    if ((int64_t)d.rows * a.hgroups * a.splits >= (1ll << 30)) return LI_ERR_UNSUPPORTED;
+    a.units = d.rows * a.hgroups * a.splits;
+    CUtensorMap qmap;
+    if (!encode_map_3d_bf16(&qmap, q, 576, d.heads, d.rows, 64)) return LI_ERR_CUDA;
+    return launch_paged_attn(qmap, a, d.cache_dtype == LI_DTYPE_E2M1, workspace, stream);
+}
+
+li_status li_paged_sparse_attention(const void* q_bf16, const void* cache, const int32_t* block_table,
+                                    const int32_t* requests_of, const int32_t* sel, int k, const li_attn_desc* desc,
+                                    void* out_bf16, void* workspace, size_t workspace_bytes, li_stream_t stream) {
+    if (!desc || k < 0 || (k > 0 && desc->rows > 0 && !sel)) return LI_ERR_INVALID_ARG;
+    PagedAttnArgs a{};
+    a.cache = cache;
+    a.table = block_table;
+    a.req = requests_of;
+    a.sel = sel;
+    a.k = k;
+    return paged_attention(q_bf16, a, *desc, k, out_bf16, workspace, workspace_bytes, stream);
+}
+
+li_status li_window_attention(const void* q_bf16, const void* cache, const int32_t* block_table,
+                              const int32_t* requests_of, const int32_t* positions, int window, int sinks, int max_len,
+                              const li_attn_desc* desc, void* out_bf16, void* workspace, size_t workspace_bytes,
+                              li_stream_t stream) {
+    if (!desc || window < 1 || sinks < 0 || max_len < 1) return LI_ERR_INVALID_ARG;
+    if ((int64_t)max_len > (int64_t)desc->max_blocks * desc->page_size) return LI_ERR_INVALID_ARG;
+    if (desc->rows > 0 && !positions) return LI_ERR_INVALID_ARG;
+    PagedAttnArgs a{};
+    a.cache = cache;
+    a.table = block_table;
+    a.req = requests_of;
+    a.pos = positions;
+    a.window = window;
+    a.sinks = sinks;
+    a.max_len = max_len;
+    const int64_t seen = (int64_t)window + sinks < max_len ? (int64_t)window + sinks : max_len;
+    return paged_attention(q_bf16, a, *desc, (int)seen, out_bf16, workspace, workspace_bytes, stream);
 }
 
 li_status li_graph_instantiate(void* graph, int use_node_priority, void** exec) {

@@ -185,6 +185,83 @@ int sparse_attn_splits(int k);
 // qmap: q as [batch * heads, 576] bf16, box 64 x 64, 128-byte swizzle
 li_status launch_sparse_attn(const CUtensorMap& qmap, SparseAttnArgs a, cudaStream_t st);
 
+// ---------------------------------------------------------------- attention over a paged cache
+struct PagedAttnArgs {
+    const void* cache;      // pages of page_size rows (4-bit rows or bf16 rows of 576)
+    const int32_t* table;   // [requests, max_blocks] pages, or nullptr: page r * max_blocks + b
+    const int32_t* req;     // [rows] request of each token (< 0: padding), or nullptr: the row itself
+    const int32_t* sel;     // selection form: [rows, k] positions, -1 = none
+    const int32_t* pos;     // window form: [rows] position of each token (< 0: padding); else nullptr
+    int rows, heads, requests, num_pages, page_size, max_blocks;
+    int k;                  // selection form
+    int window, sinks, max_len;  // window form
+    int hgroups, splits, units;  // ceil(heads / 64); CTAs per token and head group; their product with rows
+    float scale;
+    float* opart;           // [rows, splits, heads, 512] unnormalised parts (workspace; splits > 1)
+    float* mpart;           // [rows, splits, heads] maxima, log2 domain
+    float* lpart;           // [rows, splits, heads] sums of exponentials
+    __nv_bfloat16* out;     // [rows, heads, 512]
+    DevErr err;
+};
+int paged_attn_splits(int rows, int heads, int positions, int sms);
+size_t paged_attn_workspace_bytes(int rows, int heads, int splits);
+// qmap: q as [rows, heads, 576] bf16, box 64 x 64 x 1, 128-byte swizzle
+li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, bool fp4, void* workspace, cudaStream_t st);
+
+// ---------------------------------------------------------------- block tables and slot maps
+struct BlockTableArgs {
+    const int32_t* seq;     // [requests] lengths after the step
+    const int32_t* add;     // [requests] new tokens, at the end
+    int32_t* table;         // [requests, max_blocks]
+    const int32_t* pool;    // [pool_len] free pages
+    const int32_t* pool_at; // [1] first free entry of pool, or nullptr: 0
+    int requests, max_blocks, page_size, num_pages, pool_len, max_tokens;
+    int64_t* slots;         // [max_tokens]
+    int32_t* positions;     // [max_tokens]
+    int32_t* owner;         // [max_tokens]
+    int32_t* starts;        // [requests + 1]
+    int32_t* pool_next;     // [1]
+    DevErr err;
+};
+li_status launch_block_tables(const BlockTableArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- rotary positions
+constexpr int LI_ROPE_TENSORS = 4;
+struct RopeTensor {
+    const void* x;
+    void* out;
+    long long x_token, x_head, out_token, out_head;  // strides in elements
+    int heads, offset, dim;
+    int half;               // layout: pairs (i, i + rot_dim / 2) instead of (2i, 2i + 1)
+    int bf16;               // else fp32
+    int in_place;           // only the rotated part is touched
+    int end;                // work items of this tensor and those before it, per token (set by the launcher)
+    int per_head;           // items per head (set by the launcher)
+};
+struct RopeArgs {
+    RopeTensor t[LI_ROPE_TENSORS];
+    int n, tokens, rot_dim;
+    const int32_t* positions;
+    const uint64_t* turns;  // [rot_dim / 2]
+    float mscale;
+    int wide;               // 16-byte items (every address and stride allows it); else single elements
+    int items, chunk;       // per token; per CTA (set by the launcher)
+};
+li_status launch_rope(RopeArgs a, cudaStream_t st);
+
+// ---------------------------------------------------------------- the 4-bit cache
+struct Kv4Args {
+    const uint16_t* rows;   // bf16 [n, 576], row_stride elements apart (write)
+    uint16_t* out;          // bf16 [n, 576] (read)
+    uint8_t* cache;         // [num_slots] rows of LI_KV4_ROW_BYTES
+    const int64_t* slots;   // [n]
+    long long n, num_slots, row_stride;
+    int wide;               // rows are 16-byte aligned
+    DevErr err;
+};
+li_status launch_kv4_write(const Kv4Args& a, cudaStream_t st);
+li_status launch_kv4_read(const Kv4Args& a, cudaStream_t st);
+
 // ---------------------------------------------------------------- diagnostics
 li_status launch_selftest_wait(unsigned long long limit_ns, cudaStream_t st);
 
