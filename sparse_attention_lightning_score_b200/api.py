@@ -8,6 +8,7 @@ step of the indexer path runs in Python or torch.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -508,79 +509,74 @@ def li_hs_refine_fp8(c8: torch.Tensor, c_scale: torch.Tensor, cand: torch.Tensor
 
 
 # --------------------------------------------------------------------------- paged latent cache
-class _on:
-    """The device and stream of a call on tensors of `device`: `stream`, or that device's current
-    stream.  Inside, torch allocates on that stream too, so scratch memory freed when the call
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_cuda_device = torch._C._cuda_getDevice
+
+
+def _on_its_device(call):
+    """Runs a call on the device of its first tensor and on `stream`, or that device's current stream.
+    Under another stream torch allocates on that stream too, so scratch memory freed when the call
     returns is only reused behind its kernels."""
-
-    def __init__(self, device, stream):
-        self.s = stream if stream is not None else torch.cuda.current_stream(device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-        self.ptr = self.s.cuda_stream
-        self.ctx = torch.cuda.stream(stream) if stream is not None else \
-            torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.ptr
-
-    def __exit__(self, *e):
-        if self.ctx is not None:
-            self.ctx.__exit__(*e)
+    @functools.wraps(call)
+    def run(first, *args, stream=None, **kw):
+        lead = first if isinstance(first, torch.Tensor) else first[0] if first else None
+        dev = lead.device if isinstance(lead, torch.Tensor) else None
+        if dev is None or dev.type != "cuda":
+            raise ValueError(f"{call.__name__} takes CUDA tensors")
+        if stream is None and dev.index == _cuda_device():
+            return call(first, *args, **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+            return call(first, *args, **kw)
+    return run
 
 
-def _t(t, name, dtype, shape=None, device=None):
-    """Address of a contiguous CUDA tensor of this type (and shape, and device); None stays None."""
+def _t(t, name, dtype, device, shape=None):
+    """Address of a contiguous tensor of this type on this device (and of this shape); None stays None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor") from None
+    want = f"{dtype} on {device}" if shape is None else f"{dtype} {tuple(shape)} on {device}"
+    raise ValueError(f"{name} must be a contiguous {want}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+@_on_its_device
 def li_block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
                     free_pages: torch.Tensor, page_size: int, num_pages: int, max_tokens: int, *,
                     free_start: Optional[torch.Tensor] = None, slots=None, positions=None, requests=None, starts=None,
-                    free_next=None, stream=None):
+                    free_next=None):
     """Block tables and slot maps of one step: seq_lens / new_lens int32 [R] (lengths after the step, new
     tokens of each request), block_table int32 [R, max_blocks] (extended in place), free_pages int32
     [n] (taken from entry free_start[0] on) -> (slots int64 [max_tokens], positions int32
     [max_tokens], requests int32 [max_tokens], starts int32 [R + 1], free_next int32 [1]); token entries
     past the last new token are -1."""
-    dev = seq_lens.device
+    dev, i32 = seq_lens.device, torch.int32
     if block_table.dim() != 2:
         raise ValueError("block_table must be [requests, max_blocks]")
     R, blocks = block_table.shape
-    args = [_t(seq_lens, "seq_lens", torch.int32, (R,)), _t(new_lens, "new_lens", torch.int32, (R,), dev), R,
-            _t(block_table, "block_table", torch.int32, None, dev), blocks, int(page_size), int(num_pages),
-            _t(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev), free_pages.numel(),
-            _t(free_start, "free_start", torch.int32, (1,), dev), int(max_tokens)]
-    n = max(int(max_tokens), 0)
-    with _on(dev, stream) as s:
-        if slots is None:
-            slots = torch.empty(n, dtype=torch.int64, device=dev)
-        if positions is None:
-            positions = torch.empty(n, dtype=torch.int32, device=dev)
-        if requests is None:
-            requests = torch.empty(n, dtype=torch.int32, device=dev)
-        if starts is None:
-            starts = torch.empty(R + 1, dtype=torch.int32, device=dev)
-        if free_next is None:
-            free_next = torch.empty(1, dtype=torch.int32, device=dev)
-        st = _lib.load().li_block_tables(
-            *args, _t(slots, "slots", torch.int64, (n,), dev), _t(positions, "positions", torch.int32, (n,), dev),
-            _t(requests, "requests", torch.int32, (n,), dev), _t(starts, "starts", torch.int32, (R + 1,), dev),
-            _t(free_next, "free_next", torch.int32, (1,), dev), s)
+    n, n_free = max(max_tokens, 0), free_pages.numel()
+    if slots is None:
+        slots = torch.empty(n, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(n, dtype=i32, device=dev)
+    if requests is None:
+        requests = torch.empty(n, dtype=i32, device=dev)
+    if starts is None:
+        starts = torch.empty(R + 1, dtype=i32, device=dev)
+    if free_next is None:
+        free_next = torch.empty(1, dtype=i32, device=dev)
+    st = _lib.load().li_block_tables(
+        _t(seq_lens, "seq_lens", i32, dev, (R,)), _t(new_lens, "new_lens", i32, dev, (R,)), R,
+        _t(block_table, "block_table", i32, dev), blocks, page_size, num_pages,
+        _t(free_pages, "free_pages", i32, dev, (n_free,)), n_free, _t(free_start, "free_start", i32, dev, (1,)), max_tokens,
+        _t(slots, "slots", torch.int64, dev, (n,)), _t(positions, "positions", i32, dev, (n,)),
+        _t(requests, "requests", i32, dev, (n,)), _t(starts, "starts", i32, dev, (R + 1,)),
+        _t(free_next, "free_next", i32, dev, (1,)), _raw_stream(dev.index))
     if st:
         _lib.check("li_block_tables", st)
     return slots, positions, requests, starts, free_next
@@ -603,34 +599,36 @@ def li_rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
     return host.to(device)
 
 
+_ROPE_DTYPE = {torch.bfloat16: _lib.LI_DTYPE_BF16, torch.float32: _lib.LI_DTYPE_F32}
+
+
 def _rope_tensor(d, x, out, layout, offset, tokens, device):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() not in (2, 3):
-        raise ValueError("x must be CUDA tensors [tokens, heads, dim] or [tokens, dim]")
-    if x.dtype == torch.bfloat16:
-        d.dtype = _lib.LI_DTYPE_BF16
-    elif x.dtype == torch.float32:
-        d.dtype = _lib.LI_DTYPE_F32
-    else:
+    kind, lay = _ROPE_DTYPE.get(x.dtype), _ROPE_LAYOUT.get(layout)
+    if kind is None:
         raise ValueError(f"x has dtype {x.dtype}, expected bfloat16 or float32")
-    if layout not in _ROPE_LAYOUT:
+    if lay is None:
         raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
-    if x.shape[0] != tokens or x.device != device:
+    shape, xs, os = x.shape, x.stride(), out.stride()
+    if len(shape) == 3:
+        n, heads, dim = shape
+        d.x_head_stride, d.out_head_stride = xs[1], os[1]
+    elif len(shape) == 2:
+        (n, dim), heads = shape, 1
+    else:
+        raise ValueError("x must be [tokens, heads, dim] or [tokens, dim]")
+    if n != tokens or x.device != device:
         raise ValueError("x and positions must have the same tokens and device")
-    if out is not x and (out.shape != x.shape or out.dtype != x.dtype or out.device != device):
+    if out is not x and (out.shape != shape or out.dtype is not x.dtype or out.device != device):
         raise ValueError("out must have x's shape, dtype and device")
-    xs, os = x.stride(), out.stride()
     if xs[-1] != 1 or os[-1] != 1:
         raise ValueError("a head's elements must be next to each other")
-    d.x, d.out = x.data_ptr(), out.data_ptr()
-    d.x_token_stride, d.out_token_stride = xs[0], os[0]
-    three = len(xs) == 3
-    d.x_head_stride, d.out_head_stride = (xs[1], os[1]) if three else (0, 0)
-    d.heads, d.dim = (x.shape[1] if three else 1), x.shape[-1]
-    d.offset, d.layout = int(offset), _ROPE_LAYOUT[layout]
+    d.x, d.out, d.x_token_stride, d.out_token_stride = x.data_ptr(), out.data_ptr(), xs[0], os[0]
+    d.heads, d.dim, d.offset, d.layout, d.dtype = heads, dim, offset, lay, kind
 
 
+@_on_its_device
 def li_rope(x, positions: torch.Tensor, table: torch.Tensor, *, layout="interleaved", offset=0, mscale: float = 1.0,
-            out=None, stream=None):
+            out=None):
     """Rotary positions: x [tokens, heads, dim] or [tokens, dim], bf16 or fp32 (any strides over tokens and
     heads), or a list of up to four such tensors, rotated in one launch; positions int32 [tokens]
     (negative: the row of out is left as it was), table from li_rope_table.  The part [offset, offset +
@@ -639,26 +637,25 @@ def li_rope(x, positions: torch.Tensor, table: torch.Tensor, *, layout="interlea
     tensors, where padding rows are not written.  Returns out."""
     many = not isinstance(x, torch.Tensor)
     xs = list(x) if many else [x]
-    n = len(xs)
+    n, dev = len(xs), xs[0].device
     layouts = [layout] * n if isinstance(layout, str) else list(layout)
     offsets = [offset] * n if isinstance(offset, int) else list(offset)
-    if not 1 <= n <= _lib.LI_ROPE_MAX_TENSORS or len(layouts) != n or len(offsets) != n:
+    if n > _lib.LI_ROPE_MAX_TENSORS or len(layouts) != n or len(offsets) != n:
         raise ValueError("one to four tensors, with a layout and an offset each")
     if positions.dim() != 1 or table.dim() != 1:
         raise ValueError("positions and table must be one-dimensional")
-    tokens, dev = positions.shape[0], positions.device
-    pos, tab = _t(positions, "positions", torch.int32), _t(table, "table", torch.int64, None, dev)
-    with _on(dev, stream) as s:
-        if out is None:
-            outs = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in xs]
-        else:
-            outs = list(out) if many else [out]
-            if len(outs) != n:
-                raise ValueError("one out per x")
-        d = (_lib.RopeTensor * n)()
-        for i in range(n):
-            _rope_tensor(d[i], xs[i], outs[i], layouts[i], offsets[i], tokens, dev)
-        st = _lib.load().li_rope(d, n, tokens, pos, tab, 2 * table.shape[0], mscale, s)
+    tokens = positions.shape[0]
+    if out is None:
+        outs = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in xs]
+    else:
+        outs = list(out) if many else [out]
+        if len(outs) != n:
+            raise ValueError("one out per x")
+    d = (_lib.RopeTensor * n)()
+    for i in range(n):
+        _rope_tensor(d[i], xs[i], outs[i], layouts[i], offsets[i], tokens, dev)
+    st = _lib.load().li_rope(d, n, tokens, _t(positions, "positions", torch.int32, dev),
+                             _t(table, "table", torch.int64, dev), 2 * table.shape[0], mscale, _raw_stream(dev.index))
     if st:
         _lib.check("li_rope", st)
     return outs if many else outs[0]
@@ -670,37 +667,38 @@ def li_kv4_cache(num_pages: int, page_size: int, device="cuda") -> torch.Tensor:
 
 
 def _kv4_slots(cache):
-    if cache.dim() != 3 or cache.shape[2] != _lib.LI_KV4_ROW_BYTES:
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] != _lib.LI_KV4_ROW_BYTES:
         raise ValueError(f"a 4-bit cache is uint8 [pages, page_size, {_lib.LI_KV4_ROW_BYTES}]")
-    return cache.shape[0] * cache.shape[1]
+    return shape[0] * shape[1]
 
 
-def li_kv4_write(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, stream=None):
+@_on_its_device
+def li_kv4_write(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor):
     """rows bf16 [n, 576] (any row stride) quantised to 4 bits and written to `slots` int64 [n] (negative:
     skipped; no slot twice) of cache uint8 [pages, page_size, 416].  Returns cache."""
-    n = slots.shape[0]
-    if not isinstance(rows, torch.Tensor) or rows.dtype != torch.bfloat16 or rows.shape != (n, 576) or \
-            rows.device != cache.device:
-        raise ValueError("rows must be bfloat16 [n, 576] on the cache's device")
-    if n and rows.stride(1) != 1:
+    n, dev = slots.shape[0], rows.device
+    if rows.dtype is not torch.bfloat16 or rows.shape != (n, 576):
+        raise ValueError(f"rows must be bfloat16 [{n}, 576]")
+    ld, one = rows.stride()
+    if n and one != 1:
         raise ValueError("a row's elements must be next to each other")
-    num = _kv4_slots(cache)
-    at, sl = _t(cache, "cache", torch.uint8), _t(slots, "slots", torch.int64, (n,), cache.device)
-    with _on(cache.device, stream) as s:
-        st = _lib.load().li_kv4_write(rows.data_ptr(), rows.stride(0) if n > 1 else 576, sl, n, at, num, s)
+    st = _lib.load().li_kv4_write(rows.data_ptr(), ld if n > 1 else 576, _t(slots, "slots", torch.int64, dev, (n,)), n,
+                                  _t(cache, "cache", torch.uint8, dev), _kv4_slots(cache), _raw_stream(dev.index))
     if st:
         _lib.check("li_kv4_write", st)
     return cache
 
 
-def li_kv4_read(cache: torch.Tensor, slots: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None):
+@_on_its_device
+def li_kv4_read(cache: torch.Tensor, slots: torch.Tensor, *, out: Optional[torch.Tensor] = None):
     """The rows at `slots` int64 [n] of a 4-bit cache as bf16 [n, 576] (a negative slot: zeros)."""
-    n, num = slots.shape[0], _kv4_slots(cache)
-    at, sl = _t(cache, "cache", torch.uint8), _t(slots, "slots", torch.int64, (n,), cache.device)
-    with _on(cache.device, stream) as s:
-        if out is None:
-            out = torch.empty(n, 576, dtype=torch.bfloat16, device=cache.device)
-        st = _lib.load().li_kv4_read(at, num, sl, n, _t(out, "out", torch.bfloat16, (n, 576), cache.device), s)
+    n, dev = slots.shape[0], cache.device
+    if out is None:
+        out = torch.empty(n, 576, dtype=torch.bfloat16, device=dev)
+    st = _lib.load().li_kv4_read(_t(cache, "cache", torch.uint8, dev), _kv4_slots(cache),
+                                 _t(slots, "slots", torch.int64, dev, (n,)), n,
+                                 _t(out, "out", torch.bfloat16, dev, (n, 576)), _raw_stream(dev.index))
     if st:
         _lib.check("li_kv4_read", st)
     return out
@@ -716,80 +714,81 @@ def li_paged_attention_workspace(rows: int, heads: int, positions: int, device) 
 
 def _attn_desc(q, cache, block_table, requests, scale):
     """(desc, addresses of q, cache, block_table and requests) of an attention call over a paged cache."""
-    qp = _t(q, "q", torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != 576:
-        raise ValueError("q must be [rows, heads, 576]")
-    rows, heads, dev = q.shape[0], q.shape[1], q.device
-    if cache.dtype == torch.uint8:
+    dev, shape = q.device, cache.shape
+    qp = _t(q, "q", torch.bfloat16, dev)
+    if cache.dtype is torch.uint8:
         kind, width = _lib.LI_DTYPE_E2M1, _lib.LI_KV4_ROW_BYTES
     else:
         kind, width = _lib.LI_DTYPE_BF16, 576
-    cp = _t(cache, "cache", torch.uint8 if kind == _lib.LI_DTYPE_E2M1 else torch.bfloat16, None, dev)
-    if cache.dim() != 3 or cache.shape[2] != width:
+    if len(shape) != 3 or shape[2] != width:
         raise ValueError("cache must be uint8 [pages, page_size, 416] (4 bits) or bfloat16 [pages, page_size, 576]")
-    pages, size = cache.shape[0], cache.shape[1]
+    cp = _t(cache, "cache", cache.dtype if kind == _lib.LI_DTYPE_E2M1 else torch.bfloat16, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, 576]")
+    rows, heads, dim = q.shape
+    if dim != 576:
+        raise ValueError("q must be [rows, heads, 576]")
+    pages, size, _ = shape
     if block_table is None:  # a dense cache: request r's positions are page r
         tp, n_req, blocks = None, pages, 1
     else:
-        tp = _t(block_table, "block_table", torch.int32, None, dev)
+        tp = _t(block_table, "block_table", torch.int32, dev)
         if block_table.dim() != 2:
             raise ValueError("block_table must be [requests, max_blocks]")
         n_req, blocks = block_table.shape
-    rp = _t(requests, "requests", torch.int32, (rows,), dev)
+    rp = _t(requests, "requests", torch.int32, dev, (rows,))
     return _lib.AttnDesc(rows, heads, n_req, pages, size, blocks, kind, scale), qp, cp, tp, rp
 
 
+def _attn_buffers(desc, positions, out, workspace, dev):
+    """(out, workspace, its size or 0) of an attention call whose tokens see up to `positions`."""
+    rows, heads = desc.rows, desc.heads
+    if out is None:
+        out = torch.empty(rows, heads, 512, dtype=torch.bfloat16, device=dev)
+    need = _lib.load().li_paged_attention_workspace(rows, heads, positions)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif need and workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    return out, _t(out, "out", torch.bfloat16, dev, (rows, heads, 512)), workspace, need
+
+
+@_on_its_device
 def li_paged_sparse_attention(q: torch.Tensor, cache: torch.Tensor, sel: torch.Tensor, scale: float, *,
                               block_table: Optional[torch.Tensor] = None, requests: Optional[torch.Tensor] = None,
-                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                              stream=None):
+                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """li_sparse_attention over a paged cache: q bf16 [T,H,576] (any H); cache uint8 [pages, page_size, 416]
     (4 bits, li_kv4_write) or bf16 [pages, page_size, 576]; sel int32 [T,k] positions in the token's request
     (-1 = none); block_table int32 [R, max_blocks] (None: page r is request r); requests int32 [T] (None: token
     t is request t's; negative: padding, its row of out is not written) -> out bf16 [T,H,512]."""
     desc, qp, cp, tp, rp = _attn_desc(q, cache, block_table, requests, scale)
-    rows, heads, dev = q.shape[0], q.shape[1], q.device
-    k = sel.shape[-1]
-    sp = _t(sel, "sel", torch.int32, (rows, k), dev)
-    lib = _lib.load()
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(rows, heads, 512, dtype=torch.bfloat16, device=dev)
-        need = lib.li_paged_attention_workspace(rows, heads, k)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = lib.li_paged_sparse_attention(qp, cp, tp, rp, sp, k, desc,
-                                           _t(out, "out", torch.bfloat16, (rows, heads, 512), dev),
-                                           workspace.data_ptr() if need else None, need, s)
+    dev, k = q.device, sel.shape[-1]
+    sp = _t(sel, "sel", torch.int32, dev, (desc.rows, k))
+    out, op, workspace, need = _attn_buffers(desc, k, out, workspace, dev)
+    st = _lib.load().li_paged_sparse_attention(qp, cp, tp, rp, sp, k, desc, op, workspace.data_ptr() if need else None,
+                                               need, _raw_stream(dev.index))
     if st:
         _lib.check("li_paged_sparse_attention", st)
     return out
 
 
+@_on_its_device
 def li_window_attention(q: torch.Tensor, cache: torch.Tensor, positions: torch.Tensor, scale: float, window: int, *,
                         sinks: int = 0, block_table: Optional[torch.Tensor] = None,
                         requests: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
-                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Attention over a sliding window and the first `sinks` positions of a paged cache: the token at
     positions[t] = p of its request sees s <= p with s < sinks or s > p - window.  q, cache, block_table,
     requests and out as in li_paged_sparse_attention; positions int32 [T] (negative: padding, its row of out
     is not written), all below max_len (default: what the block table can hold) -> out bf16 [T,H,512]."""
     desc, qp, cp, tp, rp = _attn_desc(q, cache, block_table, requests, scale)
-    rows, heads, dev = q.shape[0], q.shape[1], q.device
-    pp = _t(positions, "positions", torch.int32, (rows,), dev)
-    if max_len is None:
-        max_len = min(desc.max_blocks * desc.page_size, 2 ** 31 - 1)
-    window, sinks, max_len = (min(int(v), 2 ** 31 - 1) for v in (window, sinks, max_len))
-    lib = _lib.load()
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(rows, heads, 512, dtype=torch.bfloat16, device=dev)
-        need = lib.li_paged_attention_workspace(rows, heads, max(min(max_len, window + sinks), 0))
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = lib.li_window_attention(qp, cp, tp, rp, pp, window, sinks, max_len, desc,
-                                     _t(out, "out", torch.bfloat16, (rows, heads, 512), dev),
-                                     workspace.data_ptr() if need else None, need, s)
+    dev, top = q.device, 2 ** 31 - 1
+    pp = _t(positions, "positions", torch.int32, dev, (desc.rows,))
+    max_len = min(desc.max_blocks * desc.page_size if max_len is None else max_len, top)
+    window, sinks = min(window, top), min(sinks, top)
+    out, op, workspace, need = _attn_buffers(desc, max(min(max_len, window + sinks), 0), out, workspace, dev)
+    st = _lib.load().li_window_attention(qp, cp, tp, rp, pp, window, sinks, max_len, desc, op,
+                                         workspace.data_ptr() if need else None, need, _raw_stream(dev.index))
     if st:
         _lib.check("li_window_attention", st)
     return out

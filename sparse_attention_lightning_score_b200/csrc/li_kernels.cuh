@@ -196,6 +196,8 @@ struct PagedAttnArgs {
     int k;                  // selection form
     int window, sinks, max_len;  // window form
     int hgroups, splits, units;  // ceil(heads / 64); CTAs per token and head group; their product with rows
+    unsigned page_mul;      // page_size as a multiplier and a shift (set by the launcher)
+    int page_shift;
     float scale;
     float* opart;           // [rows, splits, heads, 512] unnormalised parts (workspace; splits > 1)
     float* mpart;           // [rows, splits, heads] maxima, log2 domain

@@ -10,27 +10,33 @@
 // two formats share everything behind the producer warps.
 //
 // One CTA (one per SM, persistent) takes units of one token, 64 heads and a
-// share of the token's visible positions, 128 positions (a tile) at a time:
-//   - warps 0-7 (producers) hold each tile's rows once in shared memory, as bf16
-//     in nine 16 KB chunks of 64 elements x 128 positions (128-byte swizzle).
-//     A row belongs to two threads.  4 bits: a thread loads its half of the row
-//     into registers one whole tile ahead and expands it chunk by chunk; bf16:
-//     16-byte cp.async straight into the chunks.
-//   - warp 16 issues S^T = K Q^T (M = 128 positions, N = 64 heads, K = 576) and
-//     O^T += V^T P^T (M = 128 latent elements, four blocks, N = 64, K = 128),
-//     both from the same chunks: K is read K-major, V^T MN-major, so nothing is
-//     loaded or transposed a second time.  P takes the rotary chunk's place,
-//     which V does not need and whose scores are done by then.
-//   - warps 8-15 (softmax): one position per TMEM lane, 32 heads per group of four
-//     warps.  The running maximum of a head is raised only when a tile exceeds
-//     it by more than 2^8 (p stays below 2^8, which bf16 and the fp32 sums hold
-//     as exactly as p <= 1), so O is rescaled in TMEM almost never after the
-//     first tile.  Sums are kept in fp32; p is rounded to bf16 for the product
-//     (2^-9 each, the same step as the bf16 output).
-// A chunk is released as soon as its value product is done, so the next tile's
-// expansion runs under this tile's value product.
+// share of the token's visible positions, 128 positions (a tile) at a time.
+// Sixteen warps do all that is not a matrix product, in turn: they bring a tile's
+// rows into shared memory, and when its scores are done they make its weights.
+//   - Rows: each tile's rows lie once in shared memory, as bf16 in nine 16 KB chunks
+//     of 64 elements x 128 positions (128-byte swizzle), handed over in pairs.  A row
+//     belongs to four threads.  4 bits: a thread has its quarter of the row in
+//     registers one whole tile ahead (and the row's page and position one and two
+//     tiles ahead), and expands it pair by pair; bf16: 16-byte cp.async.
+//   - Weights: one position per TMEM lane, 16 heads per group of four warps.  The
+//     running maximum of a head is raised only when a tile exceeds it by more than
+//     2^8 (p stays below 2^8, which bf16 and the fp32 sums hold as exactly as
+//     p <= 1), so after a unit's first tile no maximum is exchanged and O is
+//     rescaled in TMEM almost never.  Sums are fp32; p is rounded to bf16 for the
+//     product (2^-9 each, the same step as the bf16 output).
+//   - Warp 16 issues S^T = K Q^T (M = 128 positions, N = 64 heads, K = 576) and
+//     O^T += V^T P^T (M = 128 latent elements, four blocks, N = 64, K = 128), both
+//     from the same chunks: K is read K-major, V^T MN-major, so nothing is loaded
+//     or transposed a second time.  P takes the rotary chunk's place, which V does
+//     not need and whose scores are done by then.
+// A pair is released as soon as its value product is done, so the next tile's rows
+// come in under this tile's value product.  What bounds it: at N = 64 a product
+// reads 6 KB of shared memory per 48 cycles, all that an SM has (measured: 48
+// cycles at N = 64, 64 at N = 128, where TMEM has no room for O), so the 68
+// products of a tile take 3264 cycles and everything else that touches shared
+// memory competes with them.
 // With few units the visible tiles are split over several CTAs; a second kernel
-// merges the parts (see attn_splits for the rule).
+// merges the parts (see paged_attn_splits for the rule).
 #include <cuda_fp16.h>
 
 #include "li_common.cuh"
@@ -46,25 +52,26 @@ constexpr int PA_NH = 64;                  // heads per unit (MMA N)
 constexpr int PA_M = 128;                  // positions per tile
 constexpr int PA_CH = PA_D / 64;           // 9 chunks of 64 elements
 constexpr int PA_VCH = PA_DV / 64;         // 8 of them hold the value
+constexpr int PA_PAIRS = PA_VCH / 2 + 1;   // chunks are handed over in twos (one block of V^T), the rotary one alone
 constexpr int PA_CHUNK = PA_M * 128;       // 16 KB
 constexpr int PA_QCHUNK = PA_NH * 128;     // 8 KB
-constexpr int PA_PRODUCERS = 256;
-constexpr int PA_SOFTMAX = 256;
-constexpr int PA_THREADS = PA_PRODUCERS + PA_SOFTMAX + 32;
+constexpr int PA_WORKERS = 512;            // warps 0-15
+constexpr int PA_THREADS = PA_WORKERS + 32;
+constexpr int PA_GH = 16;                  // heads per softmax group of four warps
 constexpr int PA_TMEM_COLS = 512;          // S^T: 64 columns, O^T: 4 x 64
 constexpr int PA_O_COL = 64;
-constexpr int PA_DEPTH = 4;                // bf16: chunks in flight per producer thread
 constexpr float PA_RAISE = 8.f;            // log2: a head's maximum is raised when exceeded by more
 
 constexpr int PO_Q = 0;
 constexpr int PO_K = PO_Q + PA_CH * PA_QCHUNK;
-constexpr int PO_RED = PO_K + PA_CH * PA_CHUNK;        // [2 groups][4 warps][32] fp32
-constexpr int PO_M = PO_RED + 2 * 4 * 32 * 4;          // [8 warps][32] fp32: maxima in use, later factors
-constexpr int PO_VALID = PO_M + 8 * 32 * 4;            // [2][128] bytes
-constexpr int PO_BAR = PO_VALID + 2 * PA_M;            // full[9], empty[9], qfull, sdone, pready, odone, oempty
-constexpr int PA_NBAR = 2 * PA_CH + 5;
+constexpr int PO_RED = PO_K + PA_CH * PA_CHUNK;        // [4 groups][4 warps][16] fp32
+constexpr int PO_M = PO_RED + 16 * PA_GH * 4;          // [16 warps][16] fp32: maxima in use; factors
+constexpr int PO_VALID = PO_M + 16 * PA_GH * 4;        // [2][128] bytes
+constexpr int PO_STAGE = PO_VALID + 2 * PA_M;          // [16 warps] 512 bytes: output on its way to wide stores
+constexpr int PO_BAR = PO_STAGE + 16 * 512;            // full[5], empty[5], qfull, sdone, pready, odone
+constexpr int PA_NBAR = 2 * PA_PAIRS + 4;
 constexpr int PO_TMEM = PO_BAR + PA_NBAR * 8;
-constexpr int PA_SMEM = PO_TMEM + 16 + 1024;           // + slack to align the base to 1024
+constexpr int PA_SMEM = PO_TMEM + 16;                  // the base is 1024-byte aligned (checked)
 static_assert(PA_SMEM <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ void pa_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -89,18 +96,43 @@ __device__ __forceinline__ void pa_tma_load_3d(void* dst, const void* map, int x
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 32 lanes x 16 columns (see tmem_ld32), and back.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Barrier over a group's 128 threads; group_any also returns whether any of them said yes.
+__device__ __forceinline__ void group_sync(int bar) { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ bool group_any(int bar, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(bar), "r"((uint32_t)yes)
+        : "memory");
+    return r != 0;
+}
 
 // MN-major operand with the 128-byte swizzle: each 128-byte row holds 64
 // consecutive M (or N) elements of one K index; atoms of 8 rows follow each other
@@ -115,13 +147,13 @@ __device__ __forceinline__ uint64_t pa_mnmajor_desc(uint32_t smem_addr, uint32_t
     return d;
 }
 
-// Reduce-scatter of 32 values over the warp: lane l ends with v[0] reduced for
-// index l (each step keeps the half selected by one lane bit: 31 shuffles).
+// Reduction of 16 values over the warp: lane l ends with v[0] reduced for index l % 16 (four steps keep
+// the half selected by one lane bit, the fifth joins the two halves of the warp: 16 shuffles).
 template <bool MAX>
-__device__ __forceinline__ void warp_reduce_scatter32(float (&v)[32], int lane) {
+__device__ __forceinline__ void warp_reduce_scatter16(float (&v)[16], int lane) {
 #pragma unroll
-    for (int step = 0; step < 5; ++step) {
-        const int o = 16 >> step;
+    for (int step = 0; step < 4; ++step) {
+        const int o = 8 >> step;
         const bool upper = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -131,6 +163,8 @@ __device__ __forceinline__ void warp_reduce_scatter32(float (&v)[32], int lane) 
             v[i] = MAX ? fmaxf(keep, recv) : keep + recv;
         }
     }
+    const float recv = __shfl_xor_sync(0xffffffffu, v[0], 16);
+    v[0] = MAX ? fmaxf(v[0], recv) : v[0] + recv;
 }
 
 // What a unit works on.  Entry j of a token's visible list is position j for
@@ -184,32 +218,46 @@ __device__ __forceinline__ PaUnit unit_of(const PagedAttnArgs& a, int u, bool re
     return x;
 }
 
-// Cache row of entry j of the unit's list, or null (padding, past the end, out of range).
-__device__ __forceinline__ const uint8_t* row_of(const PagedAttnArgs& a, const PaUnit& x, int j, uint32_t row_bytes) {
-    if (j >= x.n) return nullptr;
-    int s;
-    if (a.pos) {
-        s = j < x.nsink ? j : x.first + j;
-    } else {
-        s = __ldg(a.sel + (size_t)x.row * a.k + j);
-        if (s < 0) return nullptr;
-        if ((long long)s >= (long long)a.max_blocks * a.page_size) {
-            record_error(a.err, ERRBIT_BOUNDS);
-            return nullptr;
-        }
+// A tile entry on its way to a row address, one dependent load a step.
+struct PaEntry {
+    int s;              // position in the request, < 0: none
+    int req;
+    int page;           // of the cache, < 0: none
+};
+// Step 1: entry j of the unit's list.
+__device__ __forceinline__ void entry_position(const PagedAttnArgs& a, const PaUnit& x, int j, PaEntry& e) {
+    e.req = x.req;
+    e.s = -1;
+    if (j < x.n) e.s = a.pos ? (j < x.nsink ? j : x.first + j) : __ldg(a.sel + (size_t)x.row * a.k + j);
+}
+// s / page_size for 0 <= s < 2^31 (page_mul, page_shift: see page_divisor).
+__device__ __forceinline__ int block_of(const PagedAttnArgs& a, int s) {
+    return (int)(((unsigned long long)(unsigned)s * a.page_mul) >> a.page_shift);
+}
+// Step 2: its page.
+__device__ __forceinline__ void entry_page(const PagedAttnArgs& a, PaEntry& e) {
+    e.page = -1;
+    if (e.s < 0) return;
+    if ((long long)e.s >= (long long)a.max_blocks * a.page_size) {
+        record_error(a.err, ERRBIT_BOUNDS);
+        e.s = -1;
+        return;
     }
-    const int block = (int)((unsigned)s / (unsigned)a.page_size);
-    const int off = s - block * a.page_size;
-    const long long at = (long long)x.req * a.max_blocks + block;
-    const long long page = a.table ? (long long)__ldg(a.table + at) : at;
-    if (page < 0 || page >= a.num_pages) {
+    const long long at = (long long)e.req * a.max_blocks + block_of(a, e.s);
+    e.page = a.table ? __ldg(a.table + at) : (int)at;
+}
+// Step 3: its row's address, null for none.
+__device__ __forceinline__ const uint8_t* entry_row(const PagedAttnArgs& a, const PaEntry& e, uint32_t row_bytes) {
+    if (e.s < 0) return nullptr;
+    if ((unsigned)e.page >= (unsigned)a.num_pages) {
         record_error(a.err, ERRBIT_BOUNDS);
         return nullptr;
     }
-    return static_cast<const uint8_t*>(a.cache) + (page * a.page_size + off) * (long long)row_bytes;
+    const int off = e.s - block_of(a, e.s) * a.page_size;
+    return static_cast<const uint8_t*>(a.cache) + ((long long)e.page * a.page_size + off) * (long long)row_bytes;
 }
 
-// The producers' walk over the CTA's tiles.
+// A walk over the CTA's tiles.
 struct PaWalk {
     PaUnit x;
     int u, t;
@@ -236,48 +284,46 @@ struct PaWalk {
     }
 };
 
-// Eight e2m1 codes (element i in bits 4i..4i+3) times the block's scale, as four
-// bf16 pairs.  A code s.ee.m moved to bits 15 and 8..6 of a bf16 is its value
-// times 2^-126 (ee = 0 lands on the bf16 subnormals, which the multiply takes), and
-// `scale` carries the factor back up, so each product is exact: two instructions
-// to place a pair, three to mask and multiply it.
-__device__ __forceinline__ void expand8(uint32_t w, uint32_t scale, uint32_t (&o)[4]) {
-    const uint32_t lo = w << 4;  // the even codes move to the high half of their byte
-    const uint32_t sel[4] = {0x4000u, 0x5010u, 0x6020u, 0x7030u};
+// Eight e2m1 codes (element i in bits 4i..4i+3) times their block's scale, as four bf16 pairs.  The
+// product has 6 significant bits and lies between 2^-10 and 2688: exact in fp16 and in bf16.  (Placing the
+// codes' bits in bf16 with shifts and masks takes five integer instructions a pair, and the integer pipe
+// runs at half rate: 620 cycles a pair of chunks against 540 this way.)
+__device__ __forceinline__ void expand8(uint32_t w, __half2 scale, uint32_t (&o)[4]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t y = __byte_perm(lo, w, sel[i]);                   // bits 15..12: even code, 31..28: odd code
-        const uint32_t z = (y & 0x80008000u) | ((y >> 6) & 0x01C001C0u);
-        __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&z),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&scale));
+        const float2 f = __half22float2(__hmul2(*reinterpret_cast<__half2*>(&h[i]), scale));
+        __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
         o[i] = *reinterpret_cast<uint32_t*>(&p);
     }
 }
-
-// e4m3 scales (two bytes) to expand8's multipliers: the scale times 2^117 in both
-// halves of a bf16 pair (448 x 2^117 is still below bf16's largest value).  The
-// missing 2^9 stays on the whole row (the rotary part is multiplied by 2^-9, exact
-// down to bf16's subnormals) and is put back in fp32: kUp4.
-constexpr float kUp4 = 512.f;
-__device__ __forceinline__ void scales2(uint32_t two, uint32_t& s0, uint32_t& s1) {
+// Two e4m3 scales.
+__device__ __forceinline__ __half2 scales2(uint32_t two) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
-    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-    const __nv_bfloat162 a = __float2bfloat162_rn(f.x * 0x1p117f), b = __float2bfloat162_rn(f.y * 0x1p117f);
-    s0 = *reinterpret_cast<const uint32_t*>(&a);
-    s1 = *reinterpret_cast<const uint32_t*>(&b);
+    return *reinterpret_cast<__half2*>(&h);
 }
-__device__ __forceinline__ uint32_t down4(uint32_t w) {
-    const __nv_bfloat162 k = __float2bfloat162_rn(1.f / kUp4);
-    __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), k);
-    return *reinterpret_cast<uint32_t*>(&p);
+
+// bf16: hands a pair over once all but the N youngest copy groups of the thread have landed.
+template <int N>
+__device__ __forceinline__ void handed(uint64_t* full, int lane) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
 }
 
 template <bool FP4>
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const PagedAttnArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* qs = smem + PO_Q;
     uint8_t* ks = smem + PO_K;
@@ -286,24 +332,26 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     float* msm = reinterpret_cast<float*>(smem + PO_M);
     uint8_t* vflag = smem + PO_VALID;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + PO_BAR);
-    uint64_t* empty = full + PA_CH;
-    uint64_t* qfull = empty + PA_CH;
+    uint64_t* empty = full + PA_PAIRS;
+    uint64_t* qfull = empty + PA_PAIRS;
     uint64_t* sdone = qfull + 1;
     uint64_t* pready = sdone + 1;
     uint64_t* odone = pready + 1;
-    uint64_t* oempty = odone + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PO_TMEM);
 
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it; every thread sees the same address
+        if (threadIdx.x == 0) record_error(a.err, ERRBIT_BOUNDS);
+        return;
+    }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < PA_CH; ++i) {
-            mbar_init(&full[i], PA_PRODUCERS / 32);
+        for (int i = 0; i < PA_PAIRS; ++i) {
+            mbar_init(&full[i], PA_WORKERS / 32);
             mbar_init(&empty[i], 1);
         }
         mbar_init(qfull, 1);
         mbar_init(sdone, 1);
-        mbar_init(pready, PA_SOFTMAX / 32);
+        mbar_init(pready, PA_WORKERS / 32);
         mbar_init(odone, 1);
-        mbar_init(oempty, PA_SOFTMAX / 32);
         fence_mbar_init();
     }
     if (warp == 16) {
@@ -317,299 +365,388 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    if (warp < PA_PRODUCERS / 32) {
-        // ---------------------------------------------------------------- producers
-        const int r = threadIdx.x >> 1, h = threadIdx.x & 1;  // position of the tile, half of each chunk's row
-        const uint32_t k_s = smem_u32(ks);
-        uint32_t dst[4];  // the thread's four 16-byte units of a chunk
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = k_s + sw128_offset(r, 4 * h + i);
-        PaWalk w;
-        w.start(a);
-        if constexpr (FP4) {
-            uint4 code[PA_VCH], sc[2], rot[4];
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            const uint8_t* src = w.more ? row_of(a, w.x, w.t * PA_M + r, LI_KV4_ROW_BYTES) : nullptr;
-#pragma unroll
-            for (int c = 0; c < PA_VCH; ++c)
-                code[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + c * 32 + h * 16)) : z;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) sc[i] = src ? __ldg(reinterpret_cast<const uint4*>(src + 256 + i * 16)) : z;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                rot[i] = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + h * 64 + i * 16)) : z;
-            for (uint32_t n = 0; w.more; ++n) {
-                const bool valid = src != nullptr;
-                w.next(a);
-                src = w.more ? row_of(a, w.x, w.t * PA_M + r, LI_KV4_ROW_BYTES) : nullptr;
-                const uint32_t scw[8] = {sc[0].x, sc[0].y, sc[0].z, sc[0].w, sc[1].x, sc[1].y, sc[1].z, sc[1].w};
-                const uint32_t free_parity = (n & 1) ^ 1;
-                bool ok = true;
-#pragma unroll
-                for (int c = 0; c < PA_VCH; ++c) {
-                    uint32_t s0, s1;
-                    scales2((scw[c] >> (16 * h)) & 0xffffu, s0, s1);
-                    uint32_t o[4][4];
-                    expand8(code[c].x, s0, o[0]);
-                    expand8(code[c].y, s0, o[1]);
-                    expand8(code[c].z, s1, o[2]);
-                    expand8(code[c].w, s1, o[3]);
-                    code[c] = src ? __ldg(reinterpret_cast<const uint4*>(src + c * 32 + h * 16)) : z;
-                    ok = ok && mbar_wait(&empty[c], free_parity, a.err);
-                    if (c == 0 && h == 0) vflag[(n & 1) * PA_M + r] = valid ? 1 : 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        st_shared16(dst[i] + c * PA_CHUNK, o[i][0], o[i][1], o[i][2], o[i][3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[c]);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) sc[i] = src ? __ldg(reinterpret_cast<const uint4*>(src + 256 + i * 16)) : z;
-                ok = ok && mbar_wait(&empty[PA_CH - 1], free_parity, a.err);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    st_shared16(dst[i] + (PA_CH - 1) * PA_CHUNK, down4(rot[i].x), down4(rot[i].y), down4(rot[i].z),
-                                down4(rot[i].w));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[PA_CH - 1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rot[i] = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + h * 64 + i * 16)) : z;
-                if (!__all_sync(0xffffffffu, ok)) break;  // a wait ran out: the other roles' waits run out too
-            }
-        } else {
-            const uint8_t* src = w.more ? row_of(a, w.x, w.t * PA_M + r, PA_D * 2) : nullptr;
-            for (uint32_t n = 0; w.more; ++n) {
-                const uint8_t* at = src ? src + h * 64 : static_cast<const uint8_t*>(a.cache);
-                const uint32_t bytes = src ? 16u : 0u;  // 0: the unit is filled with zeros, nothing is read
-                const bool valid = src != nullptr;
-                const uint32_t free_parity = (n & 1) ^ 1;
-                bool ok = true;
-#pragma unroll
-                for (int c = 0; c < PA_CH; ++c) {
-                    ok = ok && mbar_wait(&empty[c], free_parity, a.err);
-                    if (c == 0 && h == 0) vflag[(n & 1) * PA_M + r] = valid ? 1 : 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        pa_cp_async16(dst[i] + c * PA_CHUNK, at + (src ? c * 128 + i * 16 : 0), bytes);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (c >= PA_DEPTH) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(PA_DEPTH) : "memory");
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&full[c - PA_DEPTH]);
-                    }
-                }
-                // the next tile waits for this one's products, so its last chunks are handed over first
-                w.next(a);
-                src = w.more ? row_of(a, w.x, w.t * PA_M + r, PA_D * 2) : nullptr;
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-#pragma unroll
-                    for (int c = PA_CH - PA_DEPTH; c < PA_CH; ++c) mbar_arrive(&full[c]);
-                }
-                if (!__all_sync(0xffffffffu, ok)) break;
-            }
-        }
-    } else if (warp == 16) {
+    if (warp == 16) {
         // ---------------------------------------------------------------- query loads and MMA issue
-        if (lane == 0) {
-            const uint32_t k_s = smem_u32(ks), q_s = smem_u32(qs), p_s = smem_u32(ps);
-            constexpr uint32_t IDESC_S = idesc_f32acc(PA_M, PA_NH, kFmtBF16);
-            constexpr uint32_t IDESC_O = idesc_f32acc(128, PA_NH, kFmtBF16) | (1u << 15) | (1u << 16);
-            const uint64_t keep = l2_policy_evict_last();
-            auto load_q = [&](const PaUnit& x) {
+        // The whole warp walks and waits (so that the operands stay in uniform registers); one lane issues.
+        constexpr uint32_t IDESC_S = idesc_f32acc(PA_M, PA_NH, kFmtBF16);
+        constexpr uint32_t IDESC_O = idesc_f32acc(128, PA_NH, kFmtBF16) | (1u << 15) | (1u << 16);
+        // start addresses are in units of 16 bytes in the low 14 bits and stay below 2^14: plain additions
+        const uint64_t k_desc = sw128_kmajor_desc(smem_u32(ks)), q_desc = sw128_kmajor_desc(smem_u32(qs));
+        const uint64_t v_desc = pa_mnmajor_desc(smem_u32(ks), PA_CHUNK, 1024);
+        const uint64_t p_desc = pa_mnmajor_desc(smem_u32(ps), PA_CHUNK, 1024);
+        const bool one = elect_one();
+        auto load_q = [&](const PaUnit& x) {
+            if (one) {
                 mbar_arrive_expect_tx(qfull, PA_CH * PA_QCHUNK);
                 for (int c = 0; c < PA_CH; ++c)
-                    pa_tma_load_3d(qs + c * PA_QCHUNK, &qmap, c * 64, x.hg * PA_NH, x.row, qfull, keep);
-            };
-            PaWalk w;
-            w.start(a);
-            uint32_t n = 0, units = 0, loads = 0;
-            bool ok = true;
-            if (w.more) {
-                load_q(w.x);
-                ++loads;
+                    pa_tma_load_3d(qs + c * PA_QCHUNK, &qmap, c * 64, x.hg * PA_NH, x.row, qfull,
+                                   l2_policy_evict_last());
             }
-            while (w.more && ok) {
-                ok = mbar_wait(qfull, units & 1, a.err);
-                const int tiles = w.x.t1 - w.x.t0;
-                for (int t = 0; ok && t < tiles; ++t, ++n) {
-                    const uint32_t par = n & 1;
-                    for (int c = 0; c < PA_CH; ++c) {
-                        if (!mbar_wait(&full[c], par, a.err)) { ok = false; break; }
-                        tc_fence_after();
+        };
+        PaWalk w;
+        w.start(a);
+        uint32_t n = 0, units = 0, loads = 0;
+        bool ok = true;
+        if (w.more) {
+            load_q(w.x);
+            ++loads;
+        }
+        while (w.more && ok) {
+            ok = mbar_wait(qfull, units & 1, a.err);
+            const int tiles = w.x.t1 - w.x.t0;
+            for (int t = 0; ok && t < tiles; ++t, ++n) {
+                const uint32_t par = n & 1;
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16(tmem_base, sw128_kmajor_desc(k_s + c * PA_CHUNK + kk * 32),
-                                     sw128_kmajor_desc(q_s + c * PA_QCHUNK + kk * 32), IDESC_S, (c | kk) != 0);
+                for (int p = 0; p < PA_PAIRS; ++p) {
+                    ok = ok && mbar_wait(&full[p], par, a.err);
+                    if (ok && one) {
+#pragma unroll
+                        for (int kk = 0; kk < (p < PA_PAIRS - 1 ? 8 : 4); ++kk)
+                            mma_bf16(tmem_base, k_desc + (2 * p + kk / 4) * (PA_CHUNK >> 4) + (kk & 3) * 2,
+                                     q_desc + (2 * p + kk / 4) * (PA_QCHUNK >> 4) + (kk & 3) * 2, IDESC_S, (p | kk) != 0);
                     }
-                    if (!ok) break;
-                    tc_commit(sdone);
-                    if (t == 0 && !mbar_wait(oempty, (units & 1) ^ 1, a.err)) { ok = false; break; }
-                    if (!mbar_wait(pready, par, a.err)) { ok = false; break; }
-                    tc_fence_after();
+                }
+                if (!ok) break;
+                if (one) tc_commit(sdone);
+                if (!mbar_wait(pready, par, a.err)) { ok = false; break; }  // (and the unit before has read its O)
+                tc_fence_after();
+                if (one) {
+#pragma unroll
                     for (int blk = 0; blk < PA_VCH / 2; ++blk) {
 #pragma unroll
                         for (int s = 0; s < PA_M / 16; ++s)
                             mma_bf16(tmem_base + (uint32_t)(PA_O_COL + blk * PA_NH),
-                                     pa_mnmajor_desc(k_s + 2 * blk * PA_CHUNK + s * 2048, PA_CHUNK, 1024),
-                                     pa_mnmajor_desc(p_s + s * 2048, PA_CHUNK, 1024), IDESC_O, (t | s) != 0);
-                        tc_commit(&empty[2 * blk]);
-                        tc_commit(&empty[2 * blk + 1]);
+                                     v_desc + (2 * blk * PA_CHUNK + s * 2048) / 16, p_desc + s * 2048 / 16, IDESC_O,
+                                     (t | s) != 0);
+                        tc_commit(&empty[blk]);
                     }
-                    tc_commit(&empty[PA_CH - 1]);
+                    tc_commit(&empty[PA_PAIRS - 1]);
                     if (t == tiles - 1) tc_commit(odone);
                 }
-                if (!ok) break;
-                ++units;
-                w.t = w.x.t1 - 1;
-                w.next(a);
-                if (w.more) {  // the scores of this unit are done (its last P has been made from them)
-                    load_q(w.x);
-                    ++loads;
-                }
             }
-            if (loads > units) mbar_wait(qfull, (loads - 1) & 1, a.err);  // leave no copy in flight
+            if (!ok) break;
+            ++units;
+            w.t = w.x.t1 - 1;
+            w.next(a);
+            if (w.more) {  // the scores of this unit are done (its last P has been made from them)
+                load_q(w.x);
+                ++loads;
+            }
         }
+        if (loads > units) mbar_wait(qfull, (loads - 1) & 1, a.err);  // leave no copy in flight
     } else {
-        // ---------------------------------------------------------------- softmax and output
-        const int sw = warp - PA_PRODUCERS / 32;   // 0..7
-        const int g = sw >> 2, q4 = warp & 3;      // heads 32g..32g+31; TMEM lane quarter
+        // ---------------------------------------------------------------- rows, softmax and output
+        constexpr uint32_t ROW_BYTES = FP4 ? LI_KV4_ROW_BYTES : PA_D * 2;
+        // rows: a thread's half of one chunk of each pair; eight neighbouring threads of a store share a chunk and
+        // differ in their swizzled 16-byte unit, so stores meet no bank twice
+        const int r = warp * 8 + ((lane >> 1) & 7), hi = lane >> 4, half = lane & 1;
+        // (unit 4 half + i of the row lies at dst0 ^ 16 i: the swizzle is an exclusive or of the unit)
+        const uint32_t dst0 = smem_u32(ks) + hi * PA_CHUNK + sw128_offset(r, 4 * half);
+        const uint32_t rdst0 = smem_u32(ks) + (PA_CH - 1) * PA_CHUNK + sw128_offset(r, 4 * half + 2 * hi);
+        // softmax: 16 heads of group g; q4 is the warp's quarter of the TMEM lanes
+        const int g = warp >> 2, q4 = warp & 3;
         const int row = q4 * 32 + lane;            // position of the tile; latent element of an O block
-        const uint32_t lane_base = tmem_base + ((uint32_t)(q4 * 32) << 16);
-        const float up = FP4 ? kUp4 : 1.f;
-        const float c2 = a.scale * up * 1.4426950408889634f;  // exp(x) = exp2(x log2 e)
-        float* gred = red + g * 128;
-        float* wm = msm + sw * 32;
+        const uint32_t s_at = tmem_base + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(g * PA_GH);
+        const float c2 = a.scale * 1.4426950408889634f;  // exp(x) = exp2(x log2 e)
+        float* gred = red + g * 4 * PA_GH;
+        float* wm = msm + warp * PA_GH;
         const int bar = 1 + g;
-        uint32_t n = 0, units = 0;
+
+        // Lookups run ahead of the rows, one dependent load a tile, under the score products: behind tile np the
+        // thread's part of tile np + 1 is read (4 bits), the page of np + 2 and the position of np + 3.
+        PaWalk w;
+        PaEntry e1, e2;
+        uint4 code[FP4 ? 4 : 1], rot[FP4 ? 2 : 1];
+        uint2 sc = make_uint2(0, 0);                // 4 bits: pair 2 hi + half's eight scales
+        const uint8_t* src = nullptr;               // the row of tile np
+        bool more = false;                          // tile np exists
+        uint32_t np = 0;                            // tiles brought in
         bool ok = true;
+        const auto position = [&](PaEntry& e) {     // of the next tile of the walk
+            e.s = -1;
+            e.req = w.more ? 0 : -1;                // (-1: no such tile)
+            if (w.more) {
+                entry_position(a, w.x, w.t * PA_M + r, e);
+                w.next(a);
+            }
+        };
+        auto look_ahead = [&]() {
+            more = e1.req >= 0;
+            src = entry_row(a, e1, ROW_BYTES);
+            if constexpr (FP4) {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    code[p] = src ? __ldg(reinterpret_cast<const uint4*>(src + p * 64 + hi * 32 + half * 16)) : z;
+                sc = src ? __ldg(reinterpret_cast<const uint2*>(src + 256 + (2 * hi + half) * 8)) : make_uint2(0, 0);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    rot[i] = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + (4 * half + 2 * hi + i) * 16)) : z;
+            }
+            e1 = e2;
+            entry_page(a, e1);
+            position(e2);
+        };
+        // Brings tile np in, pair by pair as the tile before releases them.
+        auto bring = [&]() {
+            const uint32_t free_parity = (np & 1) ^ 1;
+            if (hi == 0 && half == 0) vflag[(np & 1) * PA_M + r] = src ? 1 : 0;  // (last read two tiles ago)
+            if constexpr (FP4) {
+#pragma unroll
+                for (int p = 0; p < PA_PAIRS - 1; ++p) {
+                    // the pair's scales are with the row's p-th thread: hi picks the chunk, half the two blocks
+                    const int from = (lane & 14) | (p & 1) | ((p & 2) << 3);
+                    const uint32_t w0 = __shfl_sync(0xffffffffu, sc.x, from), w1 = __shfl_sync(0xffffffffu, sc.y, from);
+                    const __half2 s = scales2(((hi ? w1 : w0) >> (16 * half)) & 0xffffu);
+                    const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+                    uint32_t o[4];
+                    ok = ok && mbar_wait(&empty[p], free_parity, a.err);
+                    const uint32_t at = dst0 + 2 * p * PA_CHUNK;
+                    expand8(code[p].x, s0, o);
+                    st_shared16(at, o[0], o[1], o[2], o[3]);
+                    expand8(code[p].y, s0, o);
+                    st_shared16(at ^ 16, o[0], o[1], o[2], o[3]);
+                    expand8(code[p].z, s1, o);
+                    st_shared16(at ^ 32, o[0], o[1], o[2], o[3]);
+                    expand8(code[p].w, s1, o);
+                    st_shared16(at ^ 48, o[0], o[1], o[2], o[3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[p]);
+                }
+                ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
+                st_shared16(rdst0, rot[0].x, rot[0].y, rot[0].z, rot[0].w);
+                st_shared16(rdst0 ^ 16, rot[1].x, rot[1].y, rot[1].z, rot[1].w);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[PA_PAIRS - 1]);
+            } else {
+                const uint8_t* at = src ? src : static_cast<const uint8_t*>(a.cache);
+                const uint32_t bytes = src ? 16u : 0u;  // 0: the unit is filled with zeros, nothing is read
+                const int off = src ? hi * 128 + half * 64 : 0, step = src ? 256 : 0, unit = src ? 16 : 0;
+#pragma unroll
+                for (int p = 0; p < PA_PAIRS - 1; ++p) {
+                    ok = ok && mbar_wait(&empty[p], free_parity, a.err);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        pa_cp_async16((dst0 ^ (i << 4)) + 2 * p * PA_CHUNK, at + off + p * step + i * unit, bytes);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                }
+                ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
+                const int roff = src ? 1024 + (4 * half + 2 * hi) * 16 : 0;
+                pa_cp_async16(rdst0, at + roff, bytes);
+                pa_cp_async16(rdst0 ^ 16, at + roff + unit, bytes);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                handed<4>(&full[0], lane);
+                handed<3>(&full[1], lane);
+                handed<2>(&full[2], lane);
+                handed<1>(&full[3], lane);
+                handed<0>(&full[4], lane);
+            }
+            ++np;
+            look_ahead();
+        };
+        w.start(a);
+        if (w.more) {
+            position(e1);
+            entry_page(a, e1);
+            position(e2);
+            look_ahead();
+            bring();
+        }
+
+        uint32_t n = 0, units = 0;
         for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            const PaUnit x = unit_of(a, u, sw == 0 && lane == 0);
-            if (!x.live) continue;
-            const int split = (u / a.hgroups) % a.splits;
-            const int h0 = x.hg * PA_NH + g * 32;
-            const int nh = min(32, a.heads - h0);   // heads of this group that exist (may be <= 0)
-            const size_t part = ((size_t)x.row * a.splits + split) * a.heads + h0;
-            if (x.t0 == x.t1) {  // nothing visible in this share
+            int tiles;
+            {
+                const PaUnit x = unit_of(a, u, threadIdx.x == 0);
+                if (!x.live) continue;
+                tiles = x.t1 - x.t0;
+            }
+            // where the unit's output goes (worked out again at its end: registers are short)
+            const int h0 = (u % a.hgroups) * PA_NH + g * PA_GH;
+            const int nh = min(PA_GH, a.heads - h0);   // heads of this group that exist (may be <= 0)
+            if (tiles == 0) {  // nothing visible in this share
+                const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;
                 if (a.splits > 1) {
                     if (q4 == 0 && lane < nh) {
                         a.mpart[part + lane] = -INFINITY;
                         a.lpart[part + lane] = 0.f;
                     }
                 } else {
-                    for (int i = q4 * 32 + lane; i < nh * (PA_DV / 2); i += 128)
-                        reinterpret_cast<uint32_t*>(a.out + ((size_t)x.row * a.heads + h0) * PA_DV)[i] = 0u;
+                    for (int i = row; i < nh * (PA_DV / 2); i += 128)
+                        reinterpret_cast<uint32_t*>(a.out + part * PA_DV)[i] = 0u;  // (one part per token)
                 }
                 continue;
             }
-            float m_run = -INFINITY, l_run = 0.f;  // of head h0 + lane; l_run over this warp's positions
-            for (int t = x.t0; t < x.t1; ++t, ++n) {
-                // full[0] orders the producers' flags before this read; it stays in this phase until the
-                // tile's value product has released the chunk
+            float m_run = -INFINITY;  // of head h0 + lane % 16, the same in the group's four warps
+            float l[PA_GH];           // sums over this thread's positions, per head
+#pragma unroll
+            for (int i = 0; i < PA_GH; ++i) l[i] = 0.f;
+            for (int t = 0; t < tiles; ++t, ++n) {
+                // full[0] orders the other threads' flags before this read; it stays in this phase until the
+                // tile's value product has released the pair
                 if (!mbar_wait(&full[0], n & 1, a.err) || !mbar_wait(sdone, n & 1, a.err)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t s[32];
-                tmem_ld32(lane_base + g * 32, s);
-                tmem_ld_wait();
+                uint32_t s[PA_GH];
                 const bool valid = vflag[(n & 1) * PA_M + row] != 0;
-                float v[32];
+                bool high = t == 0;  // no maximum yet
+                if (!high) {
+                    tmem_ld16(s_at, s);
+                    tmem_ld_wait();
+                    float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = valid ? __uint_as_float(s[i]) * c2 : -INFINITY;
-                warp_reduce_scatter32<true>(v, lane);
-                gred[q4 * 32 + lane] = v[0];
-                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-                const float mx = fmaxf(fmaxf(gred[lane], gred[32 + lane]), fmaxf(gred[64 + lane], gred[96 + lane]));
-                const bool raise = mx > m_run + PA_RAISE;
-                const float m_use = raise ? mx : m_run;
-                const float f = raise && m_run != -INFINITY ? pa_ex2(m_run - m_use) : 1.f;
-                const bool rescale = __any_sync(0xffffffffu, f != 1.f);  // the same for the group's four warps
-                m_run = m_use;
-                wm[lane] = m_use == -INFINITY ? 0.f : m_use;
-                __syncwarp();
+                    for (int i = 0; i < PA_GH; i += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4*>(wm + i);
+                        const float x0 = __fmaf_rn(__uint_as_float(s[i]), c2, -m4.x);
+                        const float x1 = __fmaf_rn(__uint_as_float(s[i + 1]), c2, -m4.y);
+                        const float x2 = __fmaf_rn(__uint_as_float(s[i + 2]), c2, -m4.z);
+                        const float x3 = __fmaf_rn(__uint_as_float(s[i + 3]), c2, -m4.w);
+                        top = fmaxf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), top);
+                        s[i] = __float_as_uint(pa_ex2(x0));
+                        s[i + 1] = __float_as_uint(pa_ex2(x1));
+                        s[i + 2] = __float_as_uint(pa_ex2(x2));
+                        s[i + 3] = __float_as_uint(pa_ex2(x3));
+                    }
+                    // a position over some head's maximum by more than PA_RAISE: the group takes new ones
+                    high = group_any(bar, valid && top > PA_RAISE);
+                }
+                if (high) {
+                    float v[PA_GH];
+                    tmem_ld16(s_at, s);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4*>(wm + i);
-                    v[i] = valid ? pa_ex2(__fmaf_rn(__uint_as_float(s[i]), c2, -m4.x)) : 0.f;
-                    v[i + 1] = valid ? pa_ex2(__fmaf_rn(__uint_as_float(s[i + 1]), c2, -m4.y)) : 0.f;
-                    v[i + 2] = valid ? pa_ex2(__fmaf_rn(__uint_as_float(s[i + 2]), c2, -m4.z)) : 0.f;
-                    v[i + 3] = valid ? pa_ex2(__fmaf_rn(__uint_as_float(s[i + 3]), c2, -m4.w)) : 0.f;
+                    for (int i = 0; i < PA_GH; ++i) v[i] = valid ? __uint_as_float(s[i]) * c2 : -INFINITY;
+                    warp_reduce_scatter16<true>(v, lane);
+                    if (lane < PA_GH) gred[q4 * PA_GH + lane] = v[0];
+                    group_sync(bar);
+                    const int k = lane % PA_GH;
+                    const float mx = fmaxf(fmaxf(gred[k], gred[PA_GH + k]), fmaxf(gred[2 * PA_GH + k], gred[3 * PA_GH + k]));
+                    const bool raise = mx > m_run + PA_RAISE;
+                    const float m_use = raise ? mx : m_run;
+                    const float f = raise && m_run != -INFINITY ? pa_ex2(m_run - m_use) : 1.f;
+                    const bool rescale = __any_sync(0xffffffffu, f != 1.f);  // the same in the group's four warps
+                    m_run = m_use;
+                    if (rescale) {  // O of the tiles before is complete: its commit came before sdone's
+                        __syncwarp();
+                        if (lane < PA_GH) wm[lane] = f;
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < PA_GH; ++i) l[i] *= wm[i];
+#pragma unroll 1
+                        for (int blk = 0; blk < PA_DV / 128; ++blk) {
+                            const uint32_t at = s_at + (uint32_t)(PA_O_COL + blk * PA_NH);
+                            tmem_ld16(at, s);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < PA_GH; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * wm[i]);
+                            tmem_st16(at, s);
+                        }
+                        tmem_st_wait();
+                    }
+                    tmem_ld16(s_at, s);  // (read again rather than held: registers are short)
+                    tmem_ld_wait();
+                    __syncwarp();
+                    if (lane < PA_GH) wm[lane] = m_use == -INFINITY ? 0.f : m_use;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < PA_GH; ++i)
+                        s[i] = __float_as_uint(pa_ex2(__fmaf_rn(__uint_as_float(s[i]), c2, -wm[i])));
+                }
+                if (!__all_sync(0xffffffffu, valid)) {
+#pragma unroll
+                    for (int i = 0; i < PA_GH; ++i) s[i] = valid ? s[i] : 0u;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     uint32_t pk[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        __nv_bfloat162 pp = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                        const float p0 = __uint_as_float(s[8 * i + 2 * j]), p1 = __uint_as_float(s[8 * i + 2 * j + 1]);
+                        __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
                         pk[j] = *reinterpret_cast<uint32_t*>(&pp);
                     }
-                    *reinterpret_cast<uint4*>(ps + sw128_offset(row, 4 * g + i)) =
+                    *reinterpret_cast<uint4*>(ps + sw128_offset(row, 2 * g + i)) =
                         make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-                if (rescale) {  // O of the tiles before is complete: its commit came before sdone's
-                    __syncwarp();
-                    wm[lane] = f;
-                    __syncwarp();
-#pragma unroll 1
-                    for (int blk = 0; blk < PA_DV / 128; ++blk) {
-                        const uint32_t at = lane_base + (uint32_t)(PA_O_COL + blk * PA_NH + g * 32);
-                        tmem_ld32(at, s);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * wm[i]);
-                        tmem_st32(at, s);
-                    }
-                    tmem_st_wait();
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pready);
-                warp_reduce_scatter32<false>(v, lane);
-                l_run = l_run * f + v[0];
+#pragma unroll
+                for (int i = 0; i < PA_GH; ++i) l[i] += __uint_as_float(s[i]);
+                if (more) bring();
+                if (!ok) break;
             }
             if (!ok) break;
             if (!mbar_wait(odone, units & 1, a.err)) { ok = false; break; }
             tc_fence_after();
             ++units;
-            gred[q4 * 32 + lane] = l_run;
-            asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-            const float l = (gred[lane] + gred[32 + lane]) + (gred[64 + lane] + gred[96 + lane]);
-            asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // red is written again by the next unit
+            warp_reduce_scatter16<false>(l, lane);
+            if (lane < PA_GH) gred[q4 * PA_GH + lane] = l[0];
+            group_sync(bar);
+            const int k16 = lane % PA_GH;
+            const float sum = (gred[k16] + gred[PA_GH + k16]) + (gred[2 * PA_GH + k16] + gred[3 * PA_GH + k16]);
+            group_sync(bar);  // red is written again by the next unit
             const bool whole = a.splits == 1;
+            const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;  // [row][split][head]
             if (!whole && q4 == 0 && lane < nh) {
                 a.mpart[part + lane] = m_run;
-                a.lpart[part + lane] = l;
+                a.lpart[part + lane] = sum;
             }
-            wm[lane] = !whole ? up : l == 0.f ? 0.f : up / l;
+            if (lane < PA_GH) wm[lane] = sum == 0.f ? 0.f : 1.f / sum;
             __syncwarp();
+            // Each lane holds one latent element of 16 heads; the warp's stage turns that into 16 bytes of one
+            // head per lane.
+            uint32_t* stage = reinterpret_cast<uint32_t*>(smem + PO_STAGE) + warp * 128;
 #pragma unroll 1
             for (int blk = 0; blk < PA_DV / 128; ++blk) {
-                uint32_t s[32];
-                tmem_ld32(lane_base + (uint32_t)(PA_O_COL + blk * PA_NH + g * 32), s);
+                uint32_t s[PA_GH];
+                tmem_ld16(s_at + (uint32_t)(PA_O_COL + blk * PA_NH), s);
                 tmem_ld_wait();
-                const int d = blk * 128 + row;
+                const int d0 = blk * 128 + q4 * 32;
                 if (whole) {
-                    __nv_bfloat16* o = a.out + ((size_t)x.row * a.heads + h0) * PA_DV + d;
+                    // 8 heads at a time as bf16 pairs: stage [4 pairs][32 elements]
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < nh) o[(size_t)i * PA_DV] = __float2bfloat16_rn(__uint_as_float(s[i]) * wm[i]);
+                    for (int b8 = 0; b8 < 2; ++b8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = 8 * b8 + 2 * i;
+                            __nv_bfloat162 pp = __floats2bfloat162_rn(__uint_as_float(s[k]) * wm[k],
+                                                                      __uint_as_float(s[k + 1]) * wm[k + 1]);
+                            stage[i * 32 + lane] = *reinterpret_cast<uint32_t*>(&pp);
+                        }
+                        __syncwarp();
+                        // lanes 0-15 take the pairs' first heads, 16-31 their second: eight elements each
+                        const int pr = (lane >> 2) & 3, el = (lane & 3) * 8, k = 8 * b8 + 2 * pr + (lane >> 4);
+                        const uint4 lo = *reinterpret_cast<const uint4*>(stage + pr * 32 + el);
+                        const uint4 hi4 = *reinterpret_cast<const uint4*>(stage + pr * 32 + el + 4);
+                        const uint32_t pick = lane >> 4 ? 0x7632u : 0x5410u;
+                        if (k < nh)
+                            *reinterpret_cast<uint4*>(a.out + (part + k) * PA_DV + d0 + el) =
+                                make_uint4(__byte_perm(lo.x, lo.y, pick), __byte_perm(lo.z, lo.w, pick),
+                                           __byte_perm(hi4.x, hi4.y, pick), __byte_perm(hi4.z, hi4.w, pick));
+                        __syncwarp();
+                    }
                 } else {
-                    float* o = a.opart + part * PA_DV + d;
+                    // 4 heads at a time in fp32: stage [4 heads][32 elements]
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < nh) o[(size_t)i * PA_DV] = __uint_as_float(s[i]) * wm[i];
+                    for (int b4 = 0; b4 < 4; ++b4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            stage[i * 32 + lane] = s[4 * b4 + i];
+                        __syncwarp();
+                        const int hd = lane >> 3, el = (lane & 7) * 4, k = 4 * b4 + hd;
+                        if (k < nh)
+                            *reinterpret_cast<uint4*>(a.opart + (part + k) * PA_DV + d0 + el) =
+                                *reinterpret_cast<const uint4*>(stage + hd * 32 + el);
+                        __syncwarp();
+                    }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(oempty);
+            tc_fence_before();  // the next unit's pready hands O on
         }
+        if constexpr (!FP4) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     __syncthreads();
@@ -656,22 +793,26 @@ constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// How many CTAs share a token's tiles: the count with the least estimated time, in
-// tiles, over the waves of units the GPU runs one after another.  A unit costs its
-// tiles and about one more to fill and drain; parts cost a merge.
+// How many CTAs share a token's tiles: the count with the least estimated time, in tiles.  Units run in
+// waves of one per SM; a unit costs its tiles and about one more to fill and drain, parts cost a merge.
+// For each number of waves the largest count that fits is tried, lowered as far as the longest share
+// stays the same.
 int paged_attn_splits(int rows, int heads, int positions, int sms) {
     const long long base = (long long)rows * ((heads + PA_NH - 1) / PA_NH);
     const int tiles = (positions + PA_M - 1) / PA_M;
     int best = 1;
-    double least = 0;
-    for (int s = 1; s <= tiles && s <= 2 * sms; ++s) {
-        const long long waves = (base * s + sms - 1) / sms;
-        const double cost = (double)waves * ((tiles + s - 1) / s + 1.0) + (s > 1 ? 1.5 + 0.02 * s : 0.0);
-        if (s == 1 || cost < least) {
+    double least = (double)((base + sms - 1) / sms) * (tiles + 1.0);
+    for (int waves = 1; waves <= 4; ++waves) {
+        const long long fit = waves * (long long)sms / base;
+        if (fit < 2) continue;
+        int s = fit < tiles ? (int)fit : tiles;
+        const int share = s > 1 ? (tiles + s - 1) / s : tiles;
+        s = share > 0 ? (tiles + share - 1) / share : 1;
+        const double cost = waves * (share + 1.0) + (s > 1 ? 1.5 + 0.02 * s : 0.0);
+        if (s > 1 && cost < least) {
             best = s;
             least = cost;
         }
-        if (base * s >= 4LL * sms) break;
     }
     return best;
 }
@@ -680,6 +821,15 @@ size_t paged_attn_workspace_bytes(int rows, int heads, int splits) {
     if (splits <= 1) return 0;
     const size_t parts = (size_t)rows * splits * heads;
     return up256(parts * PA_DV * 4) + 2 * up256(parts * 4);
+}
+
+// d as a multiplier and a shift: floor(s / d) = s * ceil(2^(31+b) / d) >> (31 + b) with 2^b >= d, for every
+// 0 <= s < 2^31 (the error of the multiplier, below 2^b/2^b of a step, times s stays below 2^31/2^(31+b) <= 1/d).
+static void page_divisor(int d, unsigned* mul, int* shift) {
+    int b = 0;
+    while ((1ll << b) < d) ++b;
+    *shift = 31 + b;
+    *mul = (unsigned)(((1ull << (31 + b)) + d - 1) / d);
 }
 
 li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, bool fp4, void* workspace, cudaStream_t st) {
@@ -696,6 +846,7 @@ li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, bool fp4, 
         }
         if (dev < 64) attr_done[dev] = true;
     }
+    page_divisor(a.page_size, &a.page_mul, &a.page_shift);
     if (a.splits > 1) {
         const size_t parts = (size_t)a.rows * a.splits * a.heads;
         uint8_t* w = static_cast<uint8_t*>(workspace);
