@@ -854,7 +854,7 @@ li_status li_kv4_read(const void* cache, int64_t num_slots, const int64_t* slots
 
 size_t li_paged_attention_workspace(int rows, int heads, int positions) {
     if (rows <= 0 || heads <= 0 || positions <= 0) return 0;
-    return paged_attn_workspace_bytes(rows, heads, paged_attn_splits(rows, heads, positions, host_num_sms()));
+    return paged_attn_workspace_bytes(rows, heads, paged_attn_plan(rows, heads, positions, host_num_sms()).splits);
 }
 
 // The two forms' common checks and launch; `positions` is the longest visible list.
@@ -878,16 +878,17 @@ static li_status paged_attention(const void* q, PagedAttnArgs a, const li_attn_d
     a.max_blocks = d.max_blocks;
     a.scale = d.scale;
     a.out = static_cast<__nv_bfloat16*>(out);
-    a.hgroups = (d.heads + 63) / 64;
-    const size_t need = li_paged_attention_workspace(d.rows, d.heads, positions);
+    const PagedAttnPlan plan = paged_attn_plan(d.rows, d.heads, positions, host_num_sms());
+    a.hgroups = (d.heads + plan.heads - 1) / plan.heads;
+    a.splits = plan.splits;
+    const size_t need = paged_attn_workspace_bytes(d.rows, d.heads, plan.splits);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return LI_ERR_INVALID_ARG;
     if (ready(&a.err) != LI_OK) return LI_ERR_CUDA;
-    a.splits = positions > 0 ? paged_attn_splits(d.rows, d.heads, positions, host_num_sms()) : 1;
     if ((int64_t)d.rows * a.hgroups * a.splits >= (1ll << 30)) return LI_ERR_UNSUPPORTED;
     a.units = d.rows * a.hgroups * a.splits;
     CUtensorMap qmap;
-    if (!encode_map_3d_bf16(&qmap, q, 576, d.heads, d.rows, 64)) return LI_ERR_CUDA;
-    return launch_paged_attn(qmap, a, d.cache_dtype == LI_DTYPE_E2M1, workspace, stream);
+    if (!encode_map_3d_bf16(&qmap, q, 576, d.heads, d.rows, plan.heads)) return LI_ERR_CUDA;
+    return launch_paged_attn(qmap, a, plan.heads, d.cache_dtype == LI_DTYPE_E2M1, workspace, stream);
 }
 
 li_status li_paged_sparse_attention(const void* q_bf16, const void* cache, const int32_t* block_table,

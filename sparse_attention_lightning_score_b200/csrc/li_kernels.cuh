@@ -195,7 +195,7 @@ struct PagedAttnArgs {
     int rows, heads, requests, num_pages, page_size, max_blocks;
     int k;                  // selection form
     int window, sinks, max_len;  // window form
-    int hgroups, splits, units;  // ceil(heads / 64); CTAs per token and head group; their product with rows
+    int hgroups, splits, units;  // units of heads per token; CTAs per token and unit; their product with rows
     unsigned page_mul;      // page_size as a multiplier and a shift (set by the launcher)
     int page_shift;
     float scale;
@@ -205,10 +205,14 @@ struct PagedAttnArgs {
     __nv_bfloat16* out;     // [rows, heads, 512]
     DevErr err;
 };
-int paged_attn_splits(int rows, int heads, int positions, int sms);
+struct PagedAttnPlan {
+    int heads, splits;      // heads per unit (64, 32 or 16); CTAs that share a token's positions
+};
+PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms);
 size_t paged_attn_workspace_bytes(int rows, int heads, int splits);
-// qmap: q as [rows, heads, 576] bf16, box 64 x 64 x 1, 128-byte swizzle
-li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, bool fp4, void* workspace, cudaStream_t st);
+// qmap: q as [rows, heads, 576] bf16, box 64 x heads_per_unit x 1, 128-byte swizzle
+li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, int heads_per_unit, bool fp4, void* workspace,
+                            cudaStream_t st);
 
 // ---------------------------------------------------------------- block tables and slot maps
 struct BlockTableArgs {

@@ -48,31 +48,34 @@ namespace {
 
 constexpr int PA_D = 576;
 constexpr int PA_DV = 512;
-constexpr int PA_NH = 64;                  // heads per unit (MMA N)
 constexpr int PA_M = 128;                  // positions per tile
 constexpr int PA_CH = PA_D / 64;           // 9 chunks of 64 elements
 constexpr int PA_VCH = PA_DV / 64;         // 8 of them hold the value
 constexpr int PA_PAIRS = PA_VCH / 2 + 1;   // chunks are handed over in twos (one block of V^T), the rotary one alone
 constexpr int PA_CHUNK = PA_M * 128;       // 16 KB
-constexpr int PA_QCHUNK = PA_NH * 128;     // 8 KB
 constexpr int PA_WORKERS = 512;            // warps 0-15
 constexpr int PA_THREADS = PA_WORKERS + 32;
-constexpr int PA_GH = 16;                  // heads per softmax group of four warps
-constexpr int PA_TMEM_COLS = 512;          // S^T: 64 columns, O^T: 4 x 64
-constexpr int PA_O_COL = 64;
 constexpr float PA_RAISE = 8.f;            // log2: a head's maximum is raised when exceeded by more
 
-constexpr int PO_Q = 0;
-constexpr int PO_K = PO_Q + PA_CH * PA_QCHUNK;
-constexpr int PO_RED = PO_K + PA_CH * PA_CHUNK;        // [4 groups][4 warps][16] fp32
-constexpr int PO_M = PO_RED + 16 * PA_GH * 4;          // [16 warps][16] fp32: maxima in use; factors
-constexpr int PO_VALID = PO_M + 16 * PA_GH * 4;        // [2][128] bytes
-constexpr int PO_STAGE = PO_VALID + 2 * PA_M;          // [16 warps] 512 bytes: output on its way to wide stores
-constexpr int PO_BAR = PO_STAGE + 16 * 512;            // full[5], empty[5], qfull, sdone, pready, odone
-constexpr int PA_NBAR = 2 * PA_PAIRS + 4;
-constexpr int PO_TMEM = PO_BAR + PA_NBAR * 8;
-constexpr int PA_SMEM = PO_TMEM + 16;                  // the base is 1024-byte aligned (checked)
-static_assert(PA_SMEM <= 232448, "shared memory per CTA");
+// What depends on NH, the heads of a unit (MMA N): 64, 32 or 16.
+template <int NH>
+struct Pa {
+    static constexpr int GH = NH / 4;                     // heads per softmax group of four warps
+    static constexpr int QCHUNK = NH * 128;               // the query's 64 elements of every head
+    static constexpr int O_COL = NH;                      // TMEM: S^T in NH columns, O^T in 4 x NH
+    static constexpr int TMEM_COLS = NH == 64 ? 512 : NH == 32 ? 256 : 128;
+    static constexpr int K = PA_CH * QCHUNK;              // shared memory: query, rows, then
+    static constexpr int RED = K + PA_CH * PA_CHUNK;      // [4 groups][4 warps][GH] fp32
+    static constexpr int MAXI = RED + 16 * GH * 4;        // [16 warps][GH] fp32: maxima in use; factors
+    static constexpr int VALID = MAXI + 16 * GH * 4;      // [2][128] bytes
+    static constexpr int STAGE = VALID + 2 * PA_M;        // [4 groups] 2 KB: output on its way to whole lines
+    static constexpr int BAR = STAGE + 4 * 2048;          // full[5], empty[5], qfull, sdone, pready, odone
+    static constexpr int NBAR = 2 * PA_PAIRS + 4;
+    static constexpr int TMEM = BAR + NBAR * 8;
+    static constexpr int SMEM = TMEM + 16;                // the base is 1024-byte aligned (checked)
+};
+static_assert(Pa<64>::SMEM <= 232448, "shared memory per CTA");
+static_assert(Pa<16>::K % 1024 == 0, "the rows' swizzle atoms");
 
 __device__ __forceinline__ void pa_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -96,22 +99,33 @@ __device__ __forceinline__ void pa_tma_load_3d(void* dst, const void* map, int x
         : "memory");
 }
 
-// 32 lanes x 16 columns (see tmem_ld32), and back.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
+// 32 lanes x 4, 8 or 16 columns (see tmem_ld32), and back.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-        : "memory");
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -147,13 +161,12 @@ __device__ __forceinline__ uint64_t pa_mnmajor_desc(uint32_t smem_addr, uint32_t
     return d;
 }
 
-// Reduction of 16 values over the warp: lane l ends with v[0] reduced for index l % 16 (four steps keep
-// the half selected by one lane bit, the fifth joins the two halves of the warp: 16 shuffles).
-template <bool MAX>
-__device__ __forceinline__ void warp_reduce_scatter16(float (&v)[16], int lane) {
+// Reduction of N values over the warp: lane l ends with v[0] reduced for index l % N (log2 N steps keep
+// the half selected by one lane bit, the others join lanes that hold the same index).
+template <bool MAX, int N>
+__device__ __forceinline__ void warp_reduce_scatter(float (&v)[N], int lane) {
 #pragma unroll
-    for (int step = 0; step < 4; ++step) {
-        const int o = 8 >> step;
+    for (int o = N / 2; o > 0; o >>= 1) {
         const bool upper = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -163,8 +176,11 @@ __device__ __forceinline__ void warp_reduce_scatter16(float (&v)[16], int lane) 
             v[i] = MAX ? fmaxf(keep, recv) : keep + recv;
         }
     }
-    const float recv = __shfl_xor_sync(0xffffffffu, v[0], 16);
-    v[0] = MAX ? fmaxf(v[0], recv) : v[0] + recv;
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) {
+        const float recv = __shfl_xor_sync(0xffffffffu, v[0], o);
+        v[0] = MAX ? fmaxf(v[0], recv) : v[0] + recv;
+    }
 }
 
 // What a unit works on.  Entry j of a token's visible list is position j for
@@ -311,6 +327,19 @@ __device__ __forceinline__ __half2 scales2(uint32_t two) {
     return *reinterpret_cast<__half2*>(&h);
 }
 
+// A warp's N values of shared memory (16-byte aligned) in every lane.
+template <int N>
+__device__ __forceinline__ void read_factors(const float* m, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(m + i);
+        v[i] = x.x;
+        v[i + 1] = x.y;
+        v[i + 2] = x.z;
+        v[i + 3] = x.w;
+    }
+}
+
 // bf16: hands a pair over once all but the N youngest copy groups of the thread have landed.
 template <int N>
 __device__ __forceinline__ void handed(uint64_t* full, int lane) {
@@ -320,24 +349,26 @@ __device__ __forceinline__ void handed(uint64_t* full, int lane) {
     if (lane == 0) mbar_arrive(full);
 }
 
-template <bool FP4>
+template <bool FP4, int NH>
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const PagedAttnArgs a) {
+    using L = Pa<NH>;
+    constexpr int GH = L::GH, HB = GH < 8 ? GH : 8, PASSES = GH / HB;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* qs = smem + PO_Q;
-    uint8_t* ks = smem + PO_K;
+    uint8_t* qs = smem;
+    uint8_t* ks = smem + L::K;
     uint8_t* ps = ks + (PA_CH - 1) * PA_CHUNK;  // P over the rotary chunk
-    float* red = reinterpret_cast<float*>(smem + PO_RED);
-    float* msm = reinterpret_cast<float*>(smem + PO_M);
-    uint8_t* vflag = smem + PO_VALID;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + PO_BAR);
+    float* red = reinterpret_cast<float*>(smem + L::RED);
+    float* msm = reinterpret_cast<float*>(smem + L::MAXI);
+    uint8_t* vflag = smem + L::VALID;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR);
     uint64_t* empty = full + PA_PAIRS;
     uint64_t* qfull = empty + PA_PAIRS;
     uint64_t* sdone = qfull + 1;
     uint64_t* pready = sdone + 1;
     uint64_t* odone = pready + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PO_TMEM);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::TMEM);
 
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it; every thread sees the same address
         if (threadIdx.x == 0) record_error(a.err, ERRBIT_BOUNDS);
@@ -356,9 +387,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     }
     if (warp == 16) {
         if (lane == 0) tma_prefetch_desc(&qmap);
-        tmem_alloc(tmem_slot, PA_TMEM_COLS);
+        tmem_alloc(tmem_slot, L::TMEM_COLS);
         tmem_relinquish();
     }
+    if (a.splits > 1) pdl_trigger();  // the merge may be placed (it waits for this kernel's end)
     pdl_wait();  // the query, the selection and the cache may come from the previous kernel of the stream
     tc_fence_before();
     __syncthreads();
@@ -368,8 +400,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     if (warp == 16) {
         // ---------------------------------------------------------------- query loads and MMA issue
         // The whole warp walks and waits (so that the operands stay in uniform registers); one lane issues.
-        constexpr uint32_t IDESC_S = idesc_f32acc(PA_M, PA_NH, kFmtBF16);
-        constexpr uint32_t IDESC_O = idesc_f32acc(128, PA_NH, kFmtBF16) | (1u << 15) | (1u << 16);
+        constexpr uint32_t IDESC_S = idesc_f32acc(PA_M, NH, kFmtBF16);
+        constexpr uint32_t IDESC_O = idesc_f32acc(128, NH, kFmtBF16) | (1u << 15) | (1u << 16);
         // start addresses are in units of 16 bytes in the low 14 bits and stay below 2^14: plain additions
         const uint64_t k_desc = sw128_kmajor_desc(smem_u32(ks)), q_desc = sw128_kmajor_desc(smem_u32(qs));
         const uint64_t v_desc = pa_mnmajor_desc(smem_u32(ks), PA_CHUNK, 1024);
@@ -377,9 +409,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         const bool one = elect_one();
         auto load_q = [&](const PaUnit& x) {
             if (one) {
-                mbar_arrive_expect_tx(qfull, PA_CH * PA_QCHUNK);
+                mbar_arrive_expect_tx(qfull, PA_CH * L::QCHUNK);
                 for (int c = 0; c < PA_CH; ++c)
-                    pa_tma_load_3d(qs + c * PA_QCHUNK, &qmap, c * 64, x.hg * PA_NH, x.row, qfull,
+                    pa_tma_load_3d(qs + c * L::QCHUNK, &qmap, c * 64, x.hg * NH, x.row, qfull,
                                    l2_policy_evict_last());
             }
         };
@@ -403,7 +435,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < (p < PA_PAIRS - 1 ? 8 : 4); ++kk)
                             mma_bf16(tmem_base, k_desc + (2 * p + kk / 4) * (PA_CHUNK >> 4) + (kk & 3) * 2,
-                                     q_desc + (2 * p + kk / 4) * (PA_QCHUNK >> 4) + (kk & 3) * 2, IDESC_S, (p | kk) != 0);
+                                     q_desc + (2 * p + kk / 4) * (L::QCHUNK >> 4) + (kk & 3) * 2, IDESC_S, (p | kk) != 0);
                     }
                 }
                 if (!ok) break;
@@ -415,7 +447,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     for (int blk = 0; blk < PA_VCH / 2; ++blk) {
 #pragma unroll
                         for (int s = 0; s < PA_M / 16; ++s)
-                            mma_bf16(tmem_base + (uint32_t)(PA_O_COL + blk * PA_NH),
+                            mma_bf16(tmem_base + (uint32_t)(L::O_COL + blk * NH),
                                      v_desc + (2 * blk * PA_CHUNK + s * 2048) / 16, p_desc + s * 2048 / 16, IDESC_O,
                                      (t | s) != 0);
                         tc_commit(&empty[blk]);
@@ -443,20 +475,20 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // (unit 4 half + i of the row lies at dst0 ^ 16 i: the swizzle is an exclusive or of the unit)
         const uint32_t dst0 = smem_u32(ks) + hi * PA_CHUNK + sw128_offset(r, 4 * half);
         const uint32_t rdst0 = smem_u32(ks) + (PA_CH - 1) * PA_CHUNK + sw128_offset(r, 4 * half + 2 * hi);
-        // softmax: 16 heads of group g; q4 is the warp's quarter of the TMEM lanes
+        // softmax: GH heads of group g; q4 is the warp's quarter of the TMEM lanes
         const int g = warp >> 2, q4 = warp & 3;
         const int row = q4 * 32 + lane;            // position of the tile; latent element of an O block
-        const uint32_t s_at = tmem_base + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(g * PA_GH);
+        const uint32_t s_at = tmem_base + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(g * GH);
         const float c2 = a.scale * 1.4426950408889634f;  // exp(x) = exp2(x log2 e)
-        float* gred = red + g * 4 * PA_GH;
-        float* wm = msm + warp * PA_GH;
+        float* gred = red + g * 4 * GH;
+        float* wm = msm + warp * GH;
         const int bar = 1 + g;
 
         // Lookups run ahead of the rows, one dependent load a tile, under the score products: behind tile np the
         // thread's part of tile np + 1 is read (4 bits), the page of np + 2 and the position of np + 3.
         PaWalk w;
         PaEntry e1, e2;
-        uint4 code[FP4 ? 4 : 1], rot[FP4 ? 2 : 1];
+        uint4 code[FP4 ? 4 : 1];
         uint2 sc = make_uint2(0, 0);                // 4 bits: pair 2 hi + half's eight scales
         const uint8_t* src = nullptr;               // the row of tile np
         bool more = false;                          // tile np exists
@@ -479,9 +511,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 for (int p = 0; p < 4; ++p)
                     code[p] = src ? __ldg(reinterpret_cast<const uint4*>(src + p * 64 + hi * 32 + half * 16)) : z;
                 sc = src ? __ldg(reinterpret_cast<const uint2*>(src + 256 + (2 * hi + half) * 8)) : make_uint2(0, 0);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    rot[i] = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + (4 * half + 2 * hi + i) * 16)) : z;
             }
             e1 = e2;
             entry_page(a, e1);
@@ -492,6 +521,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             const uint32_t free_parity = (np & 1) ^ 1;
             if (hi == 0 && half == 0) vflag[(np & 1) * PA_M + r] = src ? 1 : 0;  // (last read two tiles ago)
             if constexpr (FP4) {
+                const uint4 z = make_uint4(0, 0, 0, 0);  // (the rotary part is due last: held only from here)
+                const uint4 rot0 = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + (4 * half + 2 * hi) * 16)) : z;
+                const uint4 rot1 = src ? __ldg(reinterpret_cast<const uint4*>(src + 304 + (4 * half + 2 * hi) * 16)) : z;
 #pragma unroll
                 for (int p = 0; p < PA_PAIRS - 1; ++p) {
                     // the pair's scales are with the row's p-th thread: hi picks the chunk, half the two blocks
@@ -515,8 +547,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     if (lane == 0) mbar_arrive(&full[p]);
                 }
                 ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
-                st_shared16(rdst0, rot[0].x, rot[0].y, rot[0].z, rot[0].w);
-                st_shared16(rdst0 ^ 16, rot[1].x, rot[1].y, rot[1].z, rot[1].w);
+                st_shared16(rdst0, rot0.x, rot0.y, rot0.z, rot0.w);
+                st_shared16(rdst0 ^ 16, rot1.x, rot1.y, rot1.z, rot1.w);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[PA_PAIRS - 1]);
@@ -564,8 +596,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 tiles = x.t1 - x.t0;
             }
             // where the unit's output goes (worked out again at its end: registers are short)
-            const int h0 = (u % a.hgroups) * PA_NH + g * PA_GH;
-            const int nh = min(PA_GH, a.heads - h0);   // heads of this group that exist (may be <= 0)
+            const int h0 = (u % a.hgroups) * NH + g * GH;
+            const int nh = min(GH, a.heads - h0);   // heads of this group that exist (may be <= 0)
             if (tiles == 0) {  // nothing visible in this share
                 const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;
                 if (a.splits > 1) {
@@ -579,102 +611,105 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 }
                 continue;
             }
-            float m_run = -INFINITY;  // of head h0 + lane % 16, the same in the group's four warps
-            float l[PA_GH];           // sums over this thread's positions, per head
+            float m_run[PASSES];      // of head h0 + HB pass + lane % HB, the same in the group's four warps
+            float l[GH];              // sums over this thread's positions, per head
 #pragma unroll
-            for (int i = 0; i < PA_GH; ++i) l[i] = 0.f;
+            for (int i = 0; i < PASSES; ++i) m_run[i] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < GH; ++i) l[i] = 0.f;
             for (int t = 0; t < tiles; ++t, ++n) {
                 // full[0] orders the other threads' flags before this read; it stays in this phase until the
                 // tile's value product has released the pair
                 if (!mbar_wait(&full[0], n & 1, a.err) || !mbar_wait(sdone, n & 1, a.err)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t s[PA_GH];
                 const bool valid = vflag[(n & 1) * PA_M + row] != 0;
-                bool high = t == 0;  // no maximum yet
-                if (!high) {
-                    tmem_ld16(s_at, s);
-                    tmem_ld_wait();
-                    float top = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < PA_GH; i += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4*>(wm + i);
-                        const float x0 = __fmaf_rn(__uint_as_float(s[i]), c2, -m4.x);
-                        const float x1 = __fmaf_rn(__uint_as_float(s[i + 1]), c2, -m4.y);
-                        const float x2 = __fmaf_rn(__uint_as_float(s[i + 2]), c2, -m4.z);
-                        const float x3 = __fmaf_rn(__uint_as_float(s[i + 3]), c2, -m4.w);
-                        top = fmaxf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), top);
-                        s[i] = __float_as_uint(pa_ex2(x0));
-                        s[i + 1] = __float_as_uint(pa_ex2(x1));
-                        s[i + 2] = __float_as_uint(pa_ex2(x2));
-                        s[i + 3] = __float_as_uint(pa_ex2(x3));
-                    }
-                    // a position over some head's maximum by more than PA_RAISE: the group takes new ones
-                    high = group_any(bar, valid && top > PA_RAISE);
-                }
-                if (high) {
-                    float v[PA_GH];
-                    tmem_ld16(s_at, s);
-                    tmem_ld_wait();
+                for (int ps8 = 0; ps8 < PASSES; ++ps8) {  // HB heads at a time: registers are short
+                    const uint32_t at = s_at + ps8 * HB;
+                    float* w8 = wm + ps8 * HB;
+                    uint32_t s[HB];
+                    bool high = t == 0;  // no maximum yet
+                    if (!high) {
+                        float m[HB], top = -INFINITY;
+                        tmem_ld(at, s);
+                        read_factors(w8, m);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < PA_GH; ++i) v[i] = valid ? __uint_as_float(s[i]) * c2 : -INFINITY;
-                    warp_reduce_scatter16<true>(v, lane);
-                    if (lane < PA_GH) gred[q4 * PA_GH + lane] = v[0];
-                    group_sync(bar);
-                    const int k = lane % PA_GH;
-                    const float mx = fmaxf(fmaxf(gred[k], gred[PA_GH + k]), fmaxf(gred[2 * PA_GH + k], gred[3 * PA_GH + k]));
-                    const bool raise = mx > m_run + PA_RAISE;
-                    const float m_use = raise ? mx : m_run;
-                    const float f = raise && m_run != -INFINITY ? pa_ex2(m_run - m_use) : 1.f;
-                    const bool rescale = __any_sync(0xffffffffu, f != 1.f);  // the same in the group's four warps
-                    m_run = m_use;
-                    if (rescale) {  // O of the tiles before is complete: its commit came before sdone's
-                        __syncwarp();
-                        if (lane < PA_GH) wm[lane] = f;
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < PA_GH; ++i) l[i] *= wm[i];
-#pragma unroll 1
-                        for (int blk = 0; blk < PA_DV / 128; ++blk) {
-                            const uint32_t at = s_at + (uint32_t)(PA_O_COL + blk * PA_NH);
-                            tmem_ld16(at, s);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < PA_GH; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * wm[i]);
-                            tmem_st16(at, s);
+                        for (int i = 0; i < HB; ++i) {
+                            const float x = __fmaf_rn(__uint_as_float(s[i]), c2, -m[i]);
+                            top = fmaxf(top, x);
+                            s[i] = __float_as_uint(pa_ex2(x));
                         }
-                        tmem_st_wait();
+                        // a position over some head's maximum by more than PA_RAISE: the group takes new ones
+                        high = group_any(bar, valid && top > PA_RAISE);
                     }
-                    tmem_ld16(s_at, s);  // (read again rather than held: registers are short)
-                    tmem_ld_wait();
-                    __syncwarp();
-                    if (lane < PA_GH) wm[lane] = m_use == -INFINITY ? 0.f : m_use;
-                    __syncwarp();
+                    if (high) {
+                        float v[HB];
+                        tmem_ld(at, s);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < PA_GH; ++i)
-                        s[i] = __float_as_uint(pa_ex2(__fmaf_rn(__uint_as_float(s[i]), c2, -wm[i])));
-                }
-                if (!__all_sync(0xffffffffu, valid)) {
+                        for (int i = 0; i < HB; ++i) v[i] = valid ? __uint_as_float(s[i]) * c2 : -INFINITY;
+                        warp_reduce_scatter<true>(v, lane);
+                        float* r8 = gred + ps8 * 4 * HB;
+                        if (lane < HB) r8[q4 * HB + lane] = v[0];
+                        group_sync(bar);
+                        const int k = lane % HB;
+                        const float mx = fmaxf(fmaxf(r8[k], r8[HB + k]), fmaxf(r8[2 * HB + k], r8[3 * HB + k]));
+                        const bool raise = mx > m_run[ps8] + PA_RAISE;
+                        const float m_use = raise ? mx : m_run[ps8];
+                        const float f = raise && m_run[ps8] != -INFINITY ? pa_ex2(m_run[ps8] - m_use) : 1.f;
+                        const bool rescale = __any_sync(0xffffffffu, f != 1.f);  // the same in the group's four warps
+                        m_run[ps8] = m_use;
+                        if (rescale) {  // O of the tiles before is complete: its commit came before sdone's
+                            __syncwarp();
+                            if (lane < HB) w8[lane] = f;
+                            __syncwarp();
+                            read_factors(w8, v);
 #pragma unroll
-                    for (int i = 0; i < PA_GH; ++i) s[i] = valid ? s[i] : 0u;
-                }
+                            for (int i = 0; i < HB; ++i) l[ps8 * HB + i] *= v[i];
+#pragma unroll 1
+                            for (int blk = 0; blk < PA_DV / 128; ++blk) {
+                                const uint32_t o_at = at + (uint32_t)(L::O_COL + blk * NH);
+                                tmem_ld(o_at, s);
+                                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t pk[4];
+                                for (int i = 0; i < HB; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * v[i]);
+                                tmem_st(o_at, s);
+                            }
+                            tmem_st_wait();
+                        }
+                        tmem_ld(at, s);  // (read again rather than held: registers are short)
+                        tmem_ld_wait();
+                        __syncwarp();
+                        if (lane < HB) w8[lane] = m_use == -INFINITY ? 0.f : m_use;
+                        __syncwarp();
+                        read_factors(w8, v);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float p0 = __uint_as_float(s[8 * i + 2 * j]), p1 = __uint_as_float(s[8 * i + 2 * j + 1]);
-                        __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
+                        for (int i = 0; i < HB; ++i)
+                            s[i] = __float_as_uint(pa_ex2(__fmaf_rn(__uint_as_float(s[i]), c2, -v[i])));
+                    }
+                    if (!__all_sync(0xffffffffu, valid)) {
+#pragma unroll
+                        for (int i = 0; i < HB; ++i) s[i] = valid ? s[i] : 0u;
+                    }
+                    uint32_t pk[HB / 2];
+#pragma unroll
+                    for (int j = 0; j < HB / 2; ++j) {
+                        __nv_bfloat162 pp = __floats2bfloat162_rn(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                         pk[j] = *reinterpret_cast<uint32_t*>(&pp);
                     }
-                    *reinterpret_cast<uint4*>(ps + sw128_offset(row, 2 * g + i)) =
-                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    if constexpr (HB == 8)
+                        *reinterpret_cast<uint4*>(ps + sw128_offset(row, PASSES * g + ps8)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    else
+                        *reinterpret_cast<uint2*>(ps + sw128_offset(row, g >> 1) + 8 * (g & 1)) = make_uint2(pk[0], pk[1]);
+#pragma unroll
+                    for (int i = 0; i < HB; ++i) l[ps8 * HB + i] += __uint_as_float(s[i]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pready);
-#pragma unroll
-                for (int i = 0; i < PA_GH; ++i) l[i] += __uint_as_float(s[i]);
                 if (more) bring();
                 if (!ok) break;
             }
@@ -682,66 +717,48 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             if (!mbar_wait(odone, units & 1, a.err)) { ok = false; break; }
             tc_fence_after();
             ++units;
-            warp_reduce_scatter16<false>(l, lane);
-            if (lane < PA_GH) gred[q4 * PA_GH + lane] = l[0];
+            warp_reduce_scatter<false>(l, lane);
+            if (lane < GH) gred[q4 * GH + lane] = l[0];
             group_sync(bar);
-            const int k16 = lane % PA_GH;
-            const float sum = (gred[k16] + gred[PA_GH + k16]) + (gred[2 * PA_GH + k16] + gred[3 * PA_GH + k16]);
+            const int k16 = lane % GH;
+            const float sum = (gred[k16] + gred[GH + k16]) + (gred[2 * GH + k16] + gred[3 * GH + k16]);
             group_sync(bar);  // red is written again by the next unit
             const bool whole = a.splits == 1;
             const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;  // [row][split][head]
             if (!whole && q4 == 0 && lane < nh) {
-                a.mpart[part + lane] = m_run;
+                a.mpart[part + lane] = PASSES == 1 || lane < HB ? m_run[0] : m_run[PASSES - 1];  // (lane % HB is lane's)
                 a.lpart[part + lane] = sum;
             }
-            if (lane < PA_GH) wm[lane] = sum == 0.f ? 0.f : 1.f / sum;
+            if (lane < GH) wm[lane] = sum == 0.f ? 0.f : 1.f / sum;
             __syncwarp();
-            // Each lane holds one latent element of 16 heads; the warp's stage turns that into 16 bytes of one
-            // head per lane.
-            uint32_t* stage = reinterpret_cast<uint32_t*>(smem + PO_STAGE) + warp * 128;
+            float fac[GH];
+            read_factors(wm, fac);
 #pragma unroll 1
             for (int blk = 0; blk < PA_DV / 128; ++blk) {
-                uint32_t s[PA_GH];
-                tmem_ld16(s_at + (uint32_t)(PA_O_COL + blk * PA_NH), s);
+                uint32_t s[GH];
+                tmem_ld(s_at + (uint32_t)(L::O_COL + blk * NH), s);
                 tmem_ld_wait();
-                const int d0 = blk * 128 + q4 * 32;
                 if (whole) {
-                    // 8 heads at a time as bf16 pairs: stage [4 pairs][32 elements]
+                    // Each lane holds one latent element of GH heads; the group's stage, [8 heads][128 elements] in
+                    // bf16, turns that into 16 bytes of a head's 256-byte run per thread.
+                    __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem + L::STAGE + g * 2048);
 #pragma unroll
-                    for (int b8 = 0; b8 < 2; ++b8) {
+                    for (int b8 = 0; b8 < (GH + 7) / 8; ++b8) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = 8 * b8 + 2 * i;
-                            __nv_bfloat162 pp = __floats2bfloat162_rn(__uint_as_float(s[k]) * wm[k],
-                                                                      __uint_as_float(s[k + 1]) * wm[k + 1]);
-                            stage[i * 32 + lane] = *reinterpret_cast<uint32_t*>(&pp);
-                        }
-                        __syncwarp();
-                        // lanes 0-15 take the pairs' first heads, 16-31 their second: eight elements each
-                        const int pr = (lane >> 2) & 3, el = (lane & 3) * 8, k = 8 * b8 + 2 * pr + (lane >> 4);
-                        const uint4 lo = *reinterpret_cast<const uint4*>(stage + pr * 32 + el);
-                        const uint4 hi4 = *reinterpret_cast<const uint4*>(stage + pr * 32 + el + 4);
-                        const uint32_t pick = lane >> 4 ? 0x7632u : 0x5410u;
+                        for (int i = 0; i < (GH < 8 ? GH : 8); ++i)
+                            stage[i * 128 + row] = __float2bfloat16_rn(__uint_as_float(s[8 * b8 + i]) * fac[8 * b8 + i]);
+                        group_sync(bar);
+                        const int hd = row >> 4, el = (row & 15) * 8, k = 8 * b8 + hd;  // (row: the thread of the group)
                         if (k < nh)
-                            *reinterpret_cast<uint4*>(a.out + (part + k) * PA_DV + d0 + el) =
-                                make_uint4(__byte_perm(lo.x, lo.y, pick), __byte_perm(lo.z, lo.w, pick),
-                                           __byte_perm(hi4.x, hi4.y, pick), __byte_perm(hi4.z, hi4.w, pick));
-                        __syncwarp();
+                            *reinterpret_cast<uint4*>(a.out + (part + k) * PA_DV + blk * 128 + el) =
+                                *reinterpret_cast<const uint4*>(stage + hd * 128 + el);
+                        group_sync(bar);
                     }
                 } else {
-                    // 4 heads at a time in fp32: stage [4 heads][32 elements]
+                    float* o = a.opart + part * PA_DV + blk * 128 + row;  // whole lines: 32 elements of a head a warp
 #pragma unroll
-                    for (int b4 = 0; b4 < 4; ++b4) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            stage[i * 32 + lane] = s[4 * b4 + i];
-                        __syncwarp();
-                        const int hd = lane >> 3, el = (lane & 7) * 4, k = 4 * b4 + hd;
-                        if (k < nh)
-                            *reinterpret_cast<uint4*>(a.opart + (part + k) * PA_DV + d0 + el) =
-                                *reinterpret_cast<const uint4*>(stage + hd * 32 + el);
-                        __syncwarp();
-                    }
+                    for (int i = 0; i < GH; ++i)
+                        if (i < nh) o[(size_t)i * PA_DV] = __uint_as_float(s[i]);
                 }
             }
             tc_fence_before();  // the next unit's pready hands O on
@@ -752,37 +769,78 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     __syncthreads();
     if (warp == 16) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, PA_TMEM_COLS);
+        tmem_dealloc(tmem_base, L::TMEM_COLS);
     }
 }
 
 // Merge of a token's splits: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M the
-// largest m_s (maxima are in the log2 domain).  One CTA per (head, token).
-__global__ void __launch_bounds__(128) paged_attn_merge_kernel(const PagedAttnArgs a) {
-    const int h = blockIdx.x, row = blockIdx.y;
-    const int d = threadIdx.x * 4;
+// largest m_s (maxima are in the log2 domain).  A CTA takes 512 / ST latent elements of one (head, token), four
+// to a thread, the parts dealt over its ST stripes of threads, eight in flight in each; the weights are made once in
+// shared memory.  Latency bound: an L2 read of the maxima, then the parts.  ST = 1 keeps the CTAs few (148 tokens
+// of 64 heads in 2 parts: 66 us a call against 89 with ST = 4), ST = 4 shortens the walk over many parts (74 parts
+// of 128 heads: 77 us a call against 94).
+constexpr int PA_MERGE = 128;
+template <int ST>
+__global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedAttnArgs a) {
+    constexpr int LANES = PA_MERGE / ST;
+    extern __shared__ float weight[];  // [splits]
+    __shared__ float wred[2][PA_MERGE / 32];
+    __shared__ float4 wsum[ST > 1 ? PA_MERGE : 1];
+    const int h = blockIdx.x, row = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int stripe = tid / LANES, d = blockIdx.y * (PA_DV / ST) + tid % LANES * 4;
+    pdl_wait();
     int r, p;
     if (!token_of(a, row, &r, &p, false)) return;
     const size_t at = (size_t)row * a.splits * a.heads + h;
-    float M = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.mpart[at + (size_t)s * a.heads]);
+    float top = -INFINITY;
+    for (int s = tid; s < a.splits; s += PA_MERGE) {
+        const float m = a.mpart[at + (size_t)s * a.heads];
+        weight[s] = m;
+        top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) wred[0][warp] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wred[0][0], wred[0][1]), fmaxf(wred[0][2], wred[0][3]));
+    float sum = 0.f;
+    for (int s = tid; s < a.splits; s += PA_MERGE) {
+        const float f = top == -INFINITY || weight[s] == -INFINITY ? 0.f : pa_ex2(weight[s] - top);
+        weight[s] = f;
+        if (f != 0.f) sum += f * a.lpart[at + (size_t)s * a.heads];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) wred[1][warp] = sum;
+    __syncthreads();
+    sum = (wred[1][0] + wred[1][1]) + (wred[1][2] + wred[1][3]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    if (M != -INFINITY) {
-        for (int s = 0; s < a.splits; ++s) {
-            const size_t part = at + (size_t)s * a.heads;
-            const float m = a.mpart[part];
-            if (m == -INFINITY) continue;
-            const float f = pa_ex2(m - M);
-            L += f * a.lpart[part];
-            const float4 o = *reinterpret_cast<const float4*>(a.opart + part * PA_DV + d);
-            acc.x += f * o.x;
-            acc.y += f * o.y;
-            acc.z += f * o.z;
-            acc.w += f * o.w;
+    const float* src = a.opart + at * PA_DV + d;
+#pragma unroll 8
+    for (int s = stripe; s < a.splits; s += ST) {
+        const float f = weight[s];
+        // (a part without a visible position has not been written)
+        const float4 o = f != 0.f ? *reinterpret_cast<const float4*>(src + (size_t)s * a.heads * PA_DV)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc.x += f * o.x;
+        acc.y += f * o.y;
+        acc.z += f * o.z;
+        acc.w += f * o.w;
+    }
+    if constexpr (ST > 1) {
+        wsum[tid] = acc;
+        __syncthreads();
+        if (stripe > 0) return;
+#pragma unroll
+        for (int i = 1; i < ST; ++i) {
+            const float4 o = wsum[i * LANES + tid];
+            acc.x += o.x;
+            acc.y += o.y;
+            acc.z += o.z;
+            acc.w += o.w;
         }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(a.out + ((size_t)row * a.heads + h) * PA_DV + d) =
@@ -791,27 +849,68 @@ __global__ void __launch_bounds__(128) paged_attn_merge_kernel(const PagedAttnAr
 
 constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// d as a multiplier and a shift: floor(s / d) = s * ceil(2^(31+b) / d) >> (31 + b) with 2^b >= d, for every
+// 0 <= s < 2^31 (the multiplier is less than 1 too large, which moves the quotient by less than
+// 2^31 / 2^(31+b) <= 1 / d).
+void page_divisor(int d, unsigned* mul, int* shift) {
+    int b = 0;
+    while ((1ll << b) < d) ++b;
+    *shift = 31 + b;
+    *mul = (unsigned)(((1ull << (31 + b)) + d - 1) / d);
+}
+
+template <bool FP4, int NH>
+li_status launch_units(const CUtensorMap& qmap, const PagedAttnArgs& a, cudaStream_t st) {
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_done[dev]) {
+        if (cudaFuncSetAttribute(paged_attn_kernel<FP4, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Pa<NH>::SMEM) != cudaSuccess) {
+            cudaGetLastError();
+            return LI_ERR_CUDA;
+        }
+        if (dev < 64) attr_done[dev] = true;
+    }
+    const int grid = a.units < host_num_sms() ? a.units : host_num_sms();
+    if (launch_pdl(paged_attn_kernel<FP4, NH>, dim3(grid), dim3(PA_THREADS), Pa<NH>::SMEM, st, 1, qmap, a) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return LI_ERR_CUDA;
+    }
+    return LI_OK;
+}
+
 }  // namespace
 
-// How many CTAs share a token's tiles: the count with the least estimated time, in tiles.  Units run in
-// waves of one per SM; a unit costs its tiles and about one more to fill and drain, parts cost a merge.
-// For each number of waves the largest count that fits is tried, lowered as far as the longest share
-// stays the same.
-int paged_attn_splits(int rows, int heads, int positions, int sms) {
-    const long long base = (long long)rows * ((heads + PA_NH - 1) / PA_NH);
+// How many heads a unit takes and how many CTAs share a token's tiles: the pair with the least estimated time,
+// in microseconds.  Units run in waves of one per SM; a unit costs its tiles and a start and end that grow with
+// its heads (the end writes them), parts cost a merge.  For each number of waves the largest count of splits
+// that fits is tried, lowered as far as the longest share stays the same.
+PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms) {
     const int tiles = (positions + PA_M - 1) / PA_M;
-    int best = 1;
-    double least = (double)((base + sms - 1) / sms) * (tiles + 1.0);
-    for (int waves = 1; waves <= 4; ++waves) {
-        const long long fit = waves * (long long)sms / base;
-        if (fit < 2) continue;
-        int s = fit < tiles ? (int)fit : tiles;
-        const int share = s > 1 ? (tiles + s - 1) / s : tiles;
-        s = share > 0 ? (tiles + share - 1) / share : 1;
-        const double cost = waves * (share + 1.0) + (s > 1 ? 1.5 + 0.02 * s : 0.0);
-        if (s > 1 && cost < least) {
-            best = s;
-            least = cost;
+    static const struct { int nh; float tile, unit, part; } kind[3] = {{64, 3.6f, 8.f, 2.0f}, {32, 2.95f, 7.f, 1.0f}, {16, 2.7f, 6.f, 0.5f}};
+    PagedAttnPlan best{64, 1};
+    double least = 1e30;
+    for (const auto& k : kind) {
+        const long long base = (long long)rows * ((heads + k.nh - 1) / k.nh);
+        for (int waves = 0; waves <= 4; ++waves) {  // 0: no split
+            int s = 1, share = tiles;
+            long long w = (base + sms - 1) / sms;
+            if (waves > 0) {
+                const long long fit = waves * (long long)sms / base;
+                if (fit < 2 || tiles < 2) continue;
+                s = fit < tiles ? (int)fit : tiles;
+                share = (tiles + s - 1) / s;
+                s = (tiles + share - 1) / share;
+                if (s < 2) continue;
+                w = (base * s + sms - 1) / sms;
+            }
+            const double cost = w * (share * k.tile + k.unit + (s > 1 ? k.part : 0.f)) + (s > 1 ? 4.0 + 0.02 * s : 0.0);
+            if (cost < least) {
+                least = cost;
+                best = PagedAttnPlan{k.nh, s};
+            }
         }
     }
     return best;
@@ -823,29 +922,8 @@ size_t paged_attn_workspace_bytes(int rows, int heads, int splits) {
     return up256(parts * PA_DV * 4) + 2 * up256(parts * 4);
 }
 
-// d as a multiplier and a shift: floor(s / d) = s * ceil(2^(31+b) / d) >> (31 + b) with 2^b >= d, for every
-// 0 <= s < 2^31 (the error of the multiplier, below 2^b/2^b of a step, times s stays below 2^31/2^(31+b) <= 1/d).
-static void page_divisor(int d, unsigned* mul, int* shift) {
-    int b = 0;
-    while ((1ll << b) < d) ++b;
-    *shift = 31 + b;
-    *mul = (unsigned)(((1ull << (31 + b)) + d - 1) / d);
-}
-
-li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, bool fp4, void* workspace, cudaStream_t st) {
-    static bool attr_done[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 64 || !attr_done[dev]) {
-        if (cudaFuncSetAttribute(paged_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(paged_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) !=
-                cudaSuccess) {
-            cudaGetLastError();
-            return LI_ERR_CUDA;
-        }
-        if (dev < 64) attr_done[dev] = true;
-    }
+li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, int heads_per_unit, bool fp4, void* workspace,
+                            cudaStream_t st) {
     page_divisor(a.page_size, &a.page_mul, &a.page_shift);
     if (a.splits > 1) {
         const size_t parts = (size_t)a.rows * a.splits * a.heads;
@@ -854,14 +932,26 @@ li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, bool fp4, 
         a.mpart = reinterpret_cast<float*>(w + up256(parts * PA_DV * 4));
         a.lpart = reinterpret_cast<float*>(w + up256(parts * PA_DV * 4) + up256(parts * 4));
     }
-    const int grid = a.units < host_num_sms() ? a.units : host_num_sms();
-    const cudaError_t e = fp4 ? launch_pdl(paged_attn_kernel<true>, dim3(grid), dim3(PA_THREADS), PA_SMEM, st, 1, qmap, a)
-                              : launch_pdl(paged_attn_kernel<false>, dim3(grid), dim3(PA_THREADS), PA_SMEM, st, 1, qmap, a);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return LI_ERR_CUDA;
+    li_status s;
+    if (fp4)
+        s = heads_per_unit == 64   ? launch_units<true, 64>(qmap, a, st)
+            : heads_per_unit == 32 ? launch_units<true, 32>(qmap, a, st)
+                                   : launch_units<true, 16>(qmap, a, st);
+    else
+        s = heads_per_unit == 64   ? launch_units<false, 64>(qmap, a, st)
+            : heads_per_unit == 32 ? launch_units<false, 32>(qmap, a, st)
+                                   : launch_units<false, 16>(qmap, a, st);
+    if (s != LI_OK) return s;
+    if (a.splits > 1) {
+        const size_t smem = a.splits * sizeof(float);
+        const cudaError_t e =
+            a.splits > 8 ? launch_pdl(paged_attn_merge_kernel<4>, dim3(a.heads, 4, a.rows), dim3(PA_MERGE), smem, st, 1, a)
+                          : launch_pdl(paged_attn_merge_kernel<1>, dim3(a.heads, 1, a.rows), dim3(PA_MERGE), smem, st, 1, a);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return LI_ERR_CUDA;
+        }
     }
-    if (a.splits > 1) paged_attn_merge_kernel<<<dim3(a.heads, a.rows), 128, 0, st>>>(a);
     return host_check_launch();
 }
 
