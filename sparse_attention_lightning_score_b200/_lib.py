@@ -114,6 +114,24 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+class _Binding:
+    """The functions of ``_bind.so`` (csrc/bind.cpp), loaded at the first call of one; raises if it has
+    not been built."""
+
+    def __getattr__(self, name):
+        try:
+            from . import _bind
+        except ImportError as e:
+            raise ImportError("_bind.so does not load; build it with "
+                              "`python -m sparse_attention_lightning_score_b200.build`") from e
+        _bind.set_error(LiError)
+        self.__dict__.update((n, f) for n, f in vars(_bind).items() if not n.startswith("_"))
+        return self.__dict__[name]
+
+
+bind = _Binding()
+
+
 def status_string(status: int) -> str:
     return load().li_status_string(int(status)).decode()
 

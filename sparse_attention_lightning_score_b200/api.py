@@ -3,18 +3,18 @@
 Every function takes CUDA tensors, allocates the outputs (and any workspace)
 with torch on the tensors' device, passes raw device pointers and the current
 torch stream to ``libli.so``, and raises ``LiError`` on a non-OK status.  No
-step of the indexer path runs in Python or torch.
+step of the indexer path runs in Python or torch.  The calls around the paged
+cache do the same in C++ (``csrc/bind.cpp``).
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import Optional
 
 import torch
 
 from . import _lib
-from ._lib import LiError, ScoreDesc  # noqa: F401  (re-exported)
+from ._lib import LiError, ScoreDesc, bind as _bind  # noqa: F401  (re-exported)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -509,81 +509,32 @@ def li_hs_refine_fp8(c8: torch.Tensor, c_scale: torch.Tensor, cand: torch.Tensor
 
 
 # --------------------------------------------------------------------------- paged latent cache
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_cuda_device = torch._C._cuda_getDevice
+def _under(stream, lead):
+    """The context of a call on `stream`: torch allocates on that stream too, so that scratch memory
+    freed when the call returns is only reused behind its kernels."""
+    if not isinstance(lead, torch.Tensor) or stream.device != lead.device:
+        raise ValueError("the stream and the tensors must be on the same device")
+    return torch.cuda.stream(stream)
 
 
-def _on_its_device(call):
-    """Runs a call on the device of its first tensor and on `stream`, or that device's current stream.
-    Under another stream torch allocates on that stream too, so scratch memory freed when the call
-    returns is only reused behind its kernels."""
-    @functools.wraps(call)
-    def run(first, *args, stream=None, **kw):
-        lead = first if isinstance(first, torch.Tensor) else first[0] if first else None
-        dev = lead.device if isinstance(lead, torch.Tensor) else None
-        if dev is None or dev.type != "cuda":
-            raise ValueError(f"{call.__name__} takes CUDA tensors")
-        if stream is None and dev.index == _cuda_device():
-            return call(first, *args, **kw)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-        with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
-            return call(first, *args, **kw)
-    return run
-
-
-def _t(t, name, dtype, device, shape=None):
-    """Address of a contiguous tensor of this type on this device (and of this shape); None stays None."""
-    if t is None:
-        return None
-    try:
-        if t.dtype is dtype and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape):
-            return t.data_ptr()
-    except AttributeError:
-        raise ValueError(f"{name} must be a tensor") from None
-    want = f"{dtype} on {device}" if shape is None else f"{dtype} {tuple(shape)} on {device}"
-    raise ValueError(f"{name} must be a contiguous {want}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-@_on_its_device
 def li_block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
                     free_pages: torch.Tensor, page_size: int, num_pages: int, max_tokens: int, *,
                     free_start: Optional[torch.Tensor] = None, slots=None, positions=None, requests=None, starts=None,
-                    free_next=None):
+                    free_next=None, stream=None):
     """Block tables and slot maps of one step: seq_lens / new_lens int32 [R] (lengths after the step, new
     tokens of each request), block_table int32 [R, max_blocks] (extended in place), free_pages int32
     [n] (taken from entry free_start[0] on) -> (slots int64 [max_tokens], positions int32
     [max_tokens], requests int32 [max_tokens], starts int32 [R + 1], free_next int32 [1]); token entries
     past the last new token are -1."""
-    dev, i32 = seq_lens.device, torch.int32
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [requests, max_blocks]")
-    R, blocks = block_table.shape
-    n, n_free = max(max_tokens, 0), free_pages.numel()
-    if slots is None:
-        slots = torch.empty(n, dtype=torch.int64, device=dev)
-    if positions is None:
-        positions = torch.empty(n, dtype=i32, device=dev)
-    if requests is None:
-        requests = torch.empty(n, dtype=i32, device=dev)
-    if starts is None:
-        starts = torch.empty(R + 1, dtype=i32, device=dev)
-    if free_next is None:
-        free_next = torch.empty(1, dtype=i32, device=dev)
-    st = _lib.load().li_block_tables(
-        _t(seq_lens, "seq_lens", i32, dev, (R,)), _t(new_lens, "new_lens", i32, dev, (R,)), R,
-        _t(block_table, "block_table", i32, dev), blocks, page_size, num_pages,
-        _t(free_pages, "free_pages", i32, dev, (n_free,)), n_free, _t(free_start, "free_start", i32, dev, (1,)), max_tokens,
-        _t(slots, "slots", torch.int64, dev, (n,)), _t(positions, "positions", i32, dev, (n,)),
-        _t(requests, "requests", i32, dev, (n,)), _t(starts, "starts", i32, dev, (R + 1,)),
-        _t(free_next, "free_next", i32, dev, (1,)), _raw_stream(dev.index))
-    if st:
-        _lib.check("li_block_tables", st)
-    return slots, positions, requests, starts, free_next
+    if stream is not None:
+        with _under(stream, seq_lens):
+            return _bind.block_tables(seq_lens, new_lens, block_table, free_pages, page_size, num_pages, max_tokens,
+                                      free_start, slots, positions, requests, starts, free_next)
+    return _bind.block_tables(seq_lens, new_lens, block_table, free_pages, page_size, num_pages, max_tokens, free_start,
+                              slots, positions, requests, starts, free_next)
 
 
 _ROPE_SCALING = {"none": _lib.LI_ROPE_PLAIN, "linear": _lib.LI_ROPE_LINEAR, "yarn": _lib.LI_ROPE_YARN}
-_ROPE_LAYOUT = {"interleaved": _lib.LI_ROPE_INTERLEAVED, "half": _lib.LI_ROPE_HALF}
 
 
 def li_rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -599,66 +550,23 @@ def li_rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
     return host.to(device)
 
 
-_ROPE_DTYPE = {torch.bfloat16: _lib.LI_DTYPE_BF16, torch.float32: _lib.LI_DTYPE_F32}
-
-
-def _rope_tensor(d, x, out, layout, offset, tokens, device):
-    kind, lay = _ROPE_DTYPE.get(x.dtype), _ROPE_LAYOUT.get(layout)
-    if kind is None:
-        raise ValueError(f"x has dtype {x.dtype}, expected bfloat16 or float32")
-    if lay is None:
-        raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
-    shape, xs, os = x.shape, x.stride(), out.stride()
-    if len(shape) == 3:
-        n, heads, dim = shape
-        d.x_head_stride, d.out_head_stride = xs[1], os[1]
-    elif len(shape) == 2:
-        (n, dim), heads = shape, 1
-    else:
-        raise ValueError("x must be [tokens, heads, dim] or [tokens, dim]")
-    if n != tokens or x.device != device:
-        raise ValueError("x and positions must have the same tokens and device")
-    if out is not x and (out.shape != shape or out.dtype is not x.dtype or out.device != device):
-        raise ValueError("out must have x's shape, dtype and device")
-    if xs[-1] != 1 or os[-1] != 1:
-        raise ValueError("a head's elements must be next to each other")
-    d.x, d.out, d.x_token_stride, d.out_token_stride = x.data_ptr(), out.data_ptr(), xs[0], os[0]
-    d.heads, d.dim, d.offset, d.layout, d.dtype = heads, dim, offset, lay, kind
-
-
-@_on_its_device
 def li_rope(x, positions: torch.Tensor, table: torch.Tensor, *, layout="interleaved", offset=0, mscale: float = 1.0,
-            out=None):
+            out=None, stream=None):
     """Rotary positions: x [tokens, heads, dim] or [tokens, dim], bf16 or fp32 (any strides over tokens and
     heads), or a list of up to four such tensors, rotated in one launch; positions int32 [tokens]
     (negative: the row of out is left as it was), table from li_rope_table.  The part [offset, offset +
     rot_dim) of a head turns, as pairs (2i, 2i+1) ("interleaved") or (i, i + rot_dim/2) ("half"); layout and
     offset may be lists too.  `out` (a tensor or list; x itself rotates in place) defaults to new
     tensors, where padding rows are not written.  Returns out."""
-    many = not isinstance(x, torch.Tensor)
-    xs = list(x) if many else [x]
-    n, dev = len(xs), xs[0].device
-    layouts = [layout] * n if isinstance(layout, str) else list(layout)
-    offsets = [offset] * n if isinstance(offset, int) else list(offset)
-    if n > _lib.LI_ROPE_MAX_TENSORS or len(layouts) != n or len(offsets) != n:
-        raise ValueError("one to four tensors, with a layout and an offset each")
-    if positions.dim() != 1 or table.dim() != 1:
-        raise ValueError("positions and table must be one-dimensional")
-    tokens = positions.shape[0]
-    if out is None:
-        outs = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in xs]
+    one = isinstance(x, torch.Tensor)
+    xs = [x] if one else list(x)
+    outs = None if out is None else [out] if one else list(out)
+    if stream is not None:
+        with _under(stream, xs[0] if xs else None):
+            got = _bind.rope(xs, positions, table, layout, offset, mscale, outs)
     else:
-        outs = list(out) if many else [out]
-        if len(outs) != n:
-            raise ValueError("one out per x")
-    d = (_lib.RopeTensor * n)()
-    for i in range(n):
-        _rope_tensor(d[i], xs[i], outs[i], layouts[i], offsets[i], tokens, dev)
-    st = _lib.load().li_rope(d, n, tokens, _t(positions, "positions", torch.int32, dev),
-                             _t(table, "table", torch.int64, dev), 2 * table.shape[0], mscale, _raw_stream(dev.index))
-    if st:
-        _lib.check("li_rope", st)
-    return outs if many else outs[0]
+        got = _bind.rope(xs, positions, table, layout, offset, mscale, outs)
+    return got[0] if one else got
 
 
 def li_kv4_cache(num_pages: int, page_size: int, device="cuda") -> torch.Tensor:
@@ -666,42 +574,21 @@ def li_kv4_cache(num_pages: int, page_size: int, device="cuda") -> torch.Tensor:
     return torch.zeros(num_pages, page_size, _lib.LI_KV4_ROW_BYTES, dtype=torch.uint8, device=device)
 
 
-def _kv4_slots(cache):
-    shape = cache.shape
-    if len(shape) != 3 or shape[2] != _lib.LI_KV4_ROW_BYTES:
-        raise ValueError(f"a 4-bit cache is uint8 [pages, page_size, {_lib.LI_KV4_ROW_BYTES}]")
-    return shape[0] * shape[1]
-
-
-@_on_its_device
-def li_kv4_write(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor):
+def li_kv4_write(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, stream=None):
     """rows bf16 [n, 576] (any row stride) quantised to 4 bits and written to `slots` int64 [n] (negative:
     skipped; no slot twice) of cache uint8 [pages, page_size, 416].  Returns cache."""
-    n, dev = slots.shape[0], rows.device
-    if rows.dtype is not torch.bfloat16 or rows.shape != (n, 576):
-        raise ValueError(f"rows must be bfloat16 [{n}, 576]")
-    ld, one = rows.stride()
-    if n and one != 1:
-        raise ValueError("a row's elements must be next to each other")
-    st = _lib.load().li_kv4_write(rows.data_ptr(), ld if n > 1 else 576, _t(slots, "slots", torch.int64, dev, (n,)), n,
-                                  _t(cache, "cache", torch.uint8, dev), _kv4_slots(cache), _raw_stream(dev.index))
-    if st:
-        _lib.check("li_kv4_write", st)
-    return cache
+    if stream is not None:
+        with _under(stream, rows):
+            return _bind.kv4_write(rows, slots, cache)
+    return _bind.kv4_write(rows, slots, cache)
 
 
-@_on_its_device
-def li_kv4_read(cache: torch.Tensor, slots: torch.Tensor, *, out: Optional[torch.Tensor] = None):
+def li_kv4_read(cache: torch.Tensor, slots: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None):
     """The rows at `slots` int64 [n] of a 4-bit cache as bf16 [n, 576] (a negative slot: zeros)."""
-    n, dev = slots.shape[0], cache.device
-    if out is None:
-        out = torch.empty(n, 576, dtype=torch.bfloat16, device=dev)
-    st = _lib.load().li_kv4_read(_t(cache, "cache", torch.uint8, dev), _kv4_slots(cache),
-                                 _t(slots, "slots", torch.int64, dev, (n,)), n,
-                                 _t(out, "out", torch.bfloat16, dev, (n, 576)), _raw_stream(dev.index))
-    if st:
-        _lib.check("li_kv4_read", st)
-    return out
+    if stream is not None:
+        with _under(stream, cache):
+            return _bind.kv4_read(cache, slots, out)
+    return _bind.kv4_read(cache, slots, out)
 
 
 def li_paged_attention_workspace(rows: int, heads: int, positions: int, device) -> torch.Tensor:
@@ -712,86 +599,32 @@ def li_paged_attention_workspace(rows: int, heads: int, positions: int, device) 
     return torch.empty(max(int(need), 256), dtype=torch.uint8, device=device)
 
 
-def _attn_desc(q, cache, block_table, requests, scale):
-    """(desc, addresses of q, cache, block_table and requests) of an attention call over a paged cache."""
-    dev, shape = q.device, cache.shape
-    qp = _t(q, "q", torch.bfloat16, dev)
-    if cache.dtype is torch.uint8:
-        kind, width = _lib.LI_DTYPE_E2M1, _lib.LI_KV4_ROW_BYTES
-    else:
-        kind, width = _lib.LI_DTYPE_BF16, 576
-    if len(shape) != 3 or shape[2] != width:
-        raise ValueError("cache must be uint8 [pages, page_size, 416] (4 bits) or bfloat16 [pages, page_size, 576]")
-    cp = _t(cache, "cache", cache.dtype if kind == _lib.LI_DTYPE_E2M1 else torch.bfloat16, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, heads, 576]")
-    rows, heads, dim = q.shape
-    if dim != 576:
-        raise ValueError("q must be [rows, heads, 576]")
-    pages, size, _ = shape
-    if block_table is None:  # a dense cache: request r's positions are page r
-        tp, n_req, blocks = None, pages, 1
-    else:
-        tp = _t(block_table, "block_table", torch.int32, dev)
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [requests, max_blocks]")
-        n_req, blocks = block_table.shape
-    rp = _t(requests, "requests", torch.int32, dev, (rows,))
-    return _lib.AttnDesc(rows, heads, n_req, pages, size, blocks, kind, scale), qp, cp, tp, rp
-
-
-def _attn_buffers(desc, positions, out, workspace, dev):
-    """(out, workspace, its size or 0) of an attention call whose tokens see up to `positions`."""
-    rows, heads = desc.rows, desc.heads
-    if out is None:
-        out = torch.empty(rows, heads, 512, dtype=torch.bfloat16, device=dev)
-    need = _lib.load().li_paged_attention_workspace(rows, heads, positions)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif need and workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
-    return out, _t(out, "out", torch.bfloat16, dev, (rows, heads, 512)), workspace, need
-
-
-@_on_its_device
 def li_paged_sparse_attention(q: torch.Tensor, cache: torch.Tensor, sel: torch.Tensor, scale: float, *,
                               block_table: Optional[torch.Tensor] = None, requests: Optional[torch.Tensor] = None,
-                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              stream=None):
     """li_sparse_attention over a paged cache: q bf16 [T,H,576] (any H); cache uint8 [pages, page_size, 416]
     (4 bits, li_kv4_write) or bf16 [pages, page_size, 576]; sel int32 [T,k] positions in the token's request
     (-1 = none); block_table int32 [R, max_blocks] (None: page r is request r); requests int32 [T] (None: token
     t is request t's; negative: padding, its row of out is not written) -> out bf16 [T,H,512]."""
-    desc, qp, cp, tp, rp = _attn_desc(q, cache, block_table, requests, scale)
-    dev, k = q.device, sel.shape[-1]
-    sp = _t(sel, "sel", torch.int32, dev, (desc.rows, k))
-    out, op, workspace, need = _attn_buffers(desc, k, out, workspace, dev)
-    st = _lib.load().li_paged_sparse_attention(qp, cp, tp, rp, sp, k, desc, op, workspace.data_ptr() if need else None,
-                                               need, _raw_stream(dev.index))
-    if st:
-        _lib.check("li_paged_sparse_attention", st)
-    return out
+    if stream is not None:
+        with _under(stream, q):
+            return _bind.sparse(q, cache, sel, scale, block_table, requests, out, workspace)
+    return _bind.sparse(q, cache, sel, scale, block_table, requests, out, workspace)
 
 
-@_on_its_device
 def li_window_attention(q: torch.Tensor, cache: torch.Tensor, positions: torch.Tensor, scale: float, window: int, *,
                         sinks: int = 0, block_table: Optional[torch.Tensor] = None,
                         requests: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
-                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention over a sliding window and the first `sinks` positions of a paged cache: the token at
     positions[t] = p of its request sees s <= p with s < sinks or s > p - window.  q, cache, block_table,
     requests and out as in li_paged_sparse_attention; positions int32 [T] (negative: padding, its row of out
     is not written), all below max_len (default: what the block table can hold) -> out bf16 [T,H,512]."""
-    desc, qp, cp, tp, rp = _attn_desc(q, cache, block_table, requests, scale)
-    dev, top = q.device, 2 ** 31 - 1
-    pp = _t(positions, "positions", torch.int32, dev, (desc.rows,))
-    max_len = min(desc.max_blocks * desc.page_size if max_len is None else max_len, top)
-    window, sinks = min(window, top), min(sinks, top)
-    out, op, workspace, need = _attn_buffers(desc, max(min(max_len, window + sinks), 0), out, workspace, dev)
-    st = _lib.load().li_window_attention(qp, cp, tp, rp, pp, window, sinks, max_len, desc, op,
-                                         workspace.data_ptr() if need else None, need, _raw_stream(dev.index))
-    if st:
-        _lib.check("li_window_attention", st)
-    return out
+    if stream is not None:
+        with _under(stream, q):
+            return _bind.window(q, cache, positions, scale, window, sinks, block_table, requests, max_len, out, workspace)
+    return _bind.window(q, cache, positions, scale, window, sinks, block_table, requests, max_len, out, workspace)
 
 
 def li_selftest_wait_timeout(limit_ns: int, stream=None):

@@ -6,6 +6,8 @@ Every ``csrc/*.cu`` is compiled to an object with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and the objects are
 linked into ``libli.so`` (CUDA runtime linked statically; the driver is reached
 through the runtime's entry-point query, so no libcuda link is needed).
+``csrc/bind.cpp`` is compiled against the installed torch into ``_bind.so``, the
+binding of the paged-cache calls, which calls ``libli.so`` beside it.
 """
 from __future__ import annotations
 
@@ -23,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libli.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -72,12 +76,36 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, file=sys.stderr)
 
+    bind_obj = os.path.join(BUILD_DIR, "bind.o")
+    bind = force or _stale(bind_obj, [BIND_SRC] + hdrs)
+    if bind:
+        jobs.insert(0, _bind_compile(bind_obj))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         list(ex.map(run, jobs))
     if force or jobs or _stale(LIB, objs):
         cmd = [nvcc()] + ARCH + ["-shared", "-o", LIB] + objs
         run(cmd)
+    if bind or _stale(BIND, [bind_obj]):
+        run(_bind_link(bind_obj))
     return LIB
+
+
+def _bind_compile(obj):
+    """g++ command for bind.cpp (torch's headers, its C++ ABI)."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    inc = [f"-I{d}" for d in cpp_extension.include_paths(device_type="cuda") + [sysconfig.get_path("include"), INCLUDE]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-unknown-pragmas",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + inc + ["-c", BIND_SRC, "-o", obj]
+
+
+def _bind_link(obj):
+    from torch.utils import cpp_extension
+    libs = cpp_extension.library_paths(device_type="cuda")
+    return (["g++", "-shared", "-o", BIND, obj, f"-L{PKG}", "-lli"] + [f"-L{d}" for d in libs] +
+            ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"] +
+            [f"-Wl,-rpath,{d}" for d in libs[:1]])
 
 
 def main(argv=None):
