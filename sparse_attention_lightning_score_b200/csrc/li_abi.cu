@@ -709,7 +709,7 @@ li_status li_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int 
         !aligned(free_pages, 4) || !aligned(free_start, 4))
         return LI_ERR_INVALID_ARG;
     BlockTableArgs a{seq_lens, new_lens, block_table, free_pages, free_start, requests, max_blocks, page_size,
-                     num_pages, n_free, max_tokens, slots, positions, requests_of, starts, free_next, {}};
+                     num_pages, n_free, max_tokens, slots, positions, requests_of, starts, free_next, {}, {}};
     if (ready(&a.err) != LI_OK) return LI_ERR_CUDA;
     return launch_block_tables(a, stream);
 }
@@ -757,7 +757,7 @@ li_status li_rope(const li_rope_tensor* tensors, int n_tensors, int tokens, cons
     a.positions = positions;
     a.turns = turns;
     a.mscale = mscale;
-    a.wide = 1;
+    a.wide = a.dense = 1;
     long long items = 0;
     for (int i = 0; i < n_tensors; ++i) {
         const li_rope_tensor& s = tensors[i];
@@ -787,8 +787,10 @@ li_status li_rope(const li_rope_tensor* tensors, int n_tensors, int tokens, cons
             a.wide = 0;
         items += (long long)s.heads * s.dim;
         a.t[i] = RopeTensor{s.x, s.out, s.x_token_stride, s.x_head_stride, s.out_token_stride, s.out_head_stride,
-                            s.heads, s.offset, s.dim, s.layout == LI_ROPE_HALF, bf16, in_place, 0, 0};
+                            s.heads, s.offset, s.dim, s.layout == LI_ROPE_HALF, bf16, in_place, 0, 0, 0, 0, 0, 0, {}, {}};
+        if (in_place || (s.heads > 1 && (s.x_head_stride != s.dim || s.out_head_stride != s.dim))) a.dense = 0;
     }
+    a.dense = a.dense && a.wide;
     if (items >= (1ll << 30)) return LI_ERR_UNSUPPORTED;
     if (tokens == 0) return LI_OK;
     if (!positions || !turns || !aligned(positions, 4) || !aligned(turns, 8)) return LI_ERR_INVALID_ARG;

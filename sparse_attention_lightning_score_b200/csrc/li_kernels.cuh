@@ -185,6 +185,22 @@ int sparse_attn_splits(int k);
 // qmap: q as [batch * heads, 576] bf16, box 64 x 64, 128-byte swizzle
 li_status launch_sparse_attn(const CUtensorMap& qmap, SparseAttnArgs a, cudaStream_t st);
 
+// ---------------------------------------------------------------- division by a launch constant
+// floor(s / d) = s * ceil(2^(31+b) / d) >> (31 + b) with 2^b >= d, for every 0 <= s < 2^31 and 1 <= d < 2^31: the
+// multiplier is less than 1 too large, which moves the quotient by less than 2^31 / 2^(31+b) <= 1 / d.
+struct Divisor {
+    unsigned mul;
+    int shift;
+};
+inline Divisor divisor_of(int d) {
+    int b = 0;
+    while ((1ll << b) < d) ++b;
+    return {(unsigned)(((1ull << (31 + b)) + d - 1) / d), 31 + b};
+}
+__host__ __device__ __forceinline__ int divided(int s, Divisor d) {
+    return (int)(((unsigned long long)(unsigned)s * d.mul) >> d.shift);
+}
+
 // ---------------------------------------------------------------- attention over a paged cache
 struct PagedAttnArgs {
     const void* cache;      // pages of page_size rows (4-bit rows or bf16 rows of 576)
@@ -196,8 +212,7 @@ struct PagedAttnArgs {
     int k;                  // selection form
     int window, sinks, max_len;  // window form
     int hgroups, splits, units;  // units of heads per token; CTAs per token and unit; their product with rows
-    unsigned page_mul;      // page_size as a multiplier and a shift (set by the launcher)
-    int page_shift;
+    Divisor by_page;        // page_size (set by the launcher)
     float scale;
     float* opart;           // [rows, splits, heads, 512] unnormalised parts (workspace; splits > 1)
     float* mpart;           // [rows, splits, heads] maxima, log2 domain
@@ -227,9 +242,10 @@ struct BlockTableArgs {
     int32_t* owner;         // [max_tokens]
     int32_t* starts;        // [requests + 1]
     int32_t* pool_next;     // [1]
+    Divisor by_page;        // page_size (set by the launcher)
     DevErr err;
 };
-li_status launch_block_tables(const BlockTableArgs& a, cudaStream_t st);
+li_status launch_block_tables(BlockTableArgs a, cudaStream_t st);
 
 // ---------------------------------------------------------------- rotary positions
 constexpr int LI_ROPE_TENSORS = 4;
@@ -241,8 +257,13 @@ struct RopeTensor {
     int half;               // layout: pairs (i, i + rot_dim / 2) instead of (2i, 2i + 1)
     int bf16;               // else fp32
     int in_place;           // only the rotated part is touched
-    int end;                // work items of this tensor and those before it, per token (set by the launcher)
-    int per_head;           // items per head (set by the launcher)
+    // the rest is set by the launcher
+    int rotated, per_head;  // work items of a head: the ones that rotate, all
+    int run;                // heads of a CTA's (bulk: a stage's) share
+    int chunks;             // shares of a token's heads
+    int block;              // tokens of a CTA (bulk: of a share)
+    int end;                // CTAs (bulk: shares) of this tensor and of those before it
+    Divisor by_run, by_rotated;
 };
 struct RopeArgs {
     RopeTensor t[LI_ROPE_TENSORS];
@@ -251,7 +272,7 @@ struct RopeArgs {
     const uint64_t* turns;  // [rot_dim / 2]
     float mscale;
     int wide;               // 16-byte items (every address and stride allows it); else single elements
-    int items, chunk;       // per token; per CTA (set by the launcher)
+    int dense;              // wide, every tensor out of place, and a token's heads lie side by side
 };
 li_status launch_rope(RopeArgs a, cudaStream_t st);
 

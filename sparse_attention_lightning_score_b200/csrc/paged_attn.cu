@@ -246,10 +246,6 @@ __device__ __forceinline__ void entry_position(const PagedAttnArgs& a, const PaU
     e.s = -1;
     if (j < x.n) e.s = a.pos ? (j < x.nsink ? j : x.first + j) : __ldg(a.sel + (size_t)x.row * a.k + j);
 }
-// s / page_size for 0 <= s < 2^31 (page_mul, page_shift: see page_divisor).
-__device__ __forceinline__ int block_of(const PagedAttnArgs& a, int s) {
-    return (int)(((unsigned long long)(unsigned)s * a.page_mul) >> a.page_shift);
-}
 // Step 2: its page.
 __device__ __forceinline__ void entry_page(const PagedAttnArgs& a, PaEntry& e) {
     e.page = -1;
@@ -259,7 +255,7 @@ __device__ __forceinline__ void entry_page(const PagedAttnArgs& a, PaEntry& e) {
         e.s = -1;
         return;
     }
-    const long long at = (long long)e.req * a.max_blocks + block_of(a, e.s);
+    const long long at = (long long)e.req * a.max_blocks + divided(e.s, a.by_page);
     e.page = a.table ? __ldg(a.table + at) : (int)at;
 }
 // Step 3: its row's address, null for none.
@@ -269,7 +265,7 @@ __device__ __forceinline__ const uint8_t* entry_row(const PagedAttnArgs& a, cons
         record_error(a.err, ERRBIT_BOUNDS);
         return nullptr;
     }
-    const int off = e.s - block_of(a, e.s) * a.page_size;
+    const int off = e.s - divided(e.s, a.by_page) * a.page_size;
     return static_cast<const uint8_t*>(a.cache) + ((long long)e.page * a.page_size + off) * (long long)row_bytes;
 }
 
@@ -849,16 +845,6 @@ __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedA
 
 constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// d as a multiplier and a shift: floor(s / d) = s * ceil(2^(31+b) / d) >> (31 + b) with 2^b >= d, for every
-// 0 <= s < 2^31 (the multiplier is less than 1 too large, which moves the quotient by less than
-// 2^31 / 2^(31+b) <= 1 / d).
-void page_divisor(int d, unsigned* mul, int* shift) {
-    int b = 0;
-    while ((1ll << b) < d) ++b;
-    *shift = 31 + b;
-    *mul = (unsigned)(((1ull << (31 + b)) + d - 1) / d);
-}
-
 template <bool FP4, int NH>
 li_status launch_units(const CUtensorMap& qmap, const PagedAttnArgs& a, cudaStream_t st) {
     static bool attr_done[64] = {};
@@ -924,7 +910,7 @@ size_t paged_attn_workspace_bytes(int rows, int heads, int splits) {
 
 li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, int heads_per_unit, bool fp4, void* workspace,
                             cudaStream_t st) {
-    page_divisor(a.page_size, &a.page_mul, &a.page_shift);
+    a.by_page = divisor_of(a.page_size);
     if (a.splits > 1) {
         const size_t parts = (size_t)a.rows * a.splits * a.heads;
         uint8_t* w = static_cast<uint8_t*>(workspace);

@@ -222,6 +222,35 @@ def test_rope_several_tensors_and_strides():
     assert empty.shape == (0, 4, 64) and api.li_get_last_error() == LI_OK
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_rope_many_tokens(dtype, layout):
+    """Sizes that go by bulk copies: heads that fill several stages, one head over many tokens, padding inside
+    a block of tokens; a fused buffer's rows (a token stride of their own), and the same call in place."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    n, table, freq = 3001, api.li_rope_table(64), oracle.rope_frequencies(64)
+    pos = torch.randint(0, 200000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    pos[torch.tensor([0, 7, 8, 9, 100, n - 1], device=DEV)] = -1
+    fused = torch.randn(n, 20 * 192 + 192, generator=g, device=DEV).to(dtype)
+    xs = [fused[:, :20 * 192].view(n, 20, 192), torch.randn(n, 128, generator=g, device=DEV).to(dtype),
+          torch.randn(n, 1, 64, generator=g, device=DEV).to(dtype), fused[:, 20 * 192:]]
+    offsets = [128, 0, 0, 64]
+    outs = [torch.full_like(x, 7.0, memory_format=torch.contiguous_format) for x in xs]
+    got = api.li_rope(xs, pos, table, layout=layout, offset=offsets, mscale=0.75, out=outs)
+    assert api.li_get_last_error() == LI_OK
+    some = np.r_[0:24, 90:110, 1490:1510, n - 20:n]
+    dead = (pos < 0).cpu()
+    for x, o, off in zip(xs, got, offsets):
+        assert (o.cpu()[dead] == 7).all()
+        _check_rope(o.cpu()[some], x.cpu()[some], pos.cpu().numpy()[some].tolist(), freq, layout, off, 0.75)
+        rest = lambda v: torch.cat([v[..., :off], v[..., off + 64:]], -1).cpu()[~dead]  # noqa: E731
+        assert torch.equal(rest(o), rest(x))
+    for x, o in zip(xs, got):                       # every row, against the other form
+        same = x.clone()
+        api.li_rope(same, pos, table, layout=layout, offset=offsets[[id(v) for v in xs].index(id(x))], mscale=0.75, out=same)
+        assert torch.equal(same[~dead.to(DEV)], o[~dead.to(DEV)])
+
+
 def test_rope_refusals():
     table, pos = api.li_rope_table(64), _i32([1, 2])
     x = torch.zeros(2, 4, 128, device=DEV)
