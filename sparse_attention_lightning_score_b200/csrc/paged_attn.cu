@@ -17,7 +17,9 @@
 //     of 64 elements x 128 positions (128-byte swizzle), handed over in pairs.  A row
 //     belongs to four threads.  4 bits: a thread has its quarter of the row in
 //     registers one whole tile ahead (and the row's page and position one and two
-//     tiles ahead), and expands it pair by pair; bf16: 16-byte cp.async.
+//     tiles ahead), and expands it pair by pair; bf16: the copy engine gathers four
+//     rows of a chunk at a time (16-byte cp.async by the threads kept the
+//     load-store unit busy for 4000 cycles a tile).
 //   - Weights: one position per TMEM lane, 16 heads per group of four warps.  The
 //     running maximum of a head is raised only when a tile exceeds it by more than
 //     2^8 (p stays below 2^8, which bf16 and the fp32 sums hold as exactly as
@@ -77,8 +79,15 @@ struct Pa {
 static_assert(Pa<64>::SMEM <= 232448, "shared memory per CTA");
 static_assert(Pa<16>::K % 1024 == 0, "the rows' swizzle atoms");
 
-__device__ __forceinline__ void pa_cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+// 64 elements (from x) of four rows of a bf16 cache, 128 bytes each, side by side at dst in the swizzled layout;
+// a row past the end reads as zeros.  The map's box is one row high.
+__device__ __forceinline__ void pa_gather4(uint32_t dst, const void* map, int x, const int (&row)[4], uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
+        "r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ float pa_ex2(float x) {
     float y;
@@ -258,15 +267,14 @@ __device__ __forceinline__ void entry_page(const PagedAttnArgs& a, PaEntry& e) {
     const long long at = (long long)e.req * a.max_blocks + divided(e.s, a.by_page);
     e.page = a.table ? __ldg(a.table + at) : (int)at;
 }
-// Step 3: its row's address, null for none.
-__device__ __forceinline__ const uint8_t* entry_row(const PagedAttnArgs& a, const PaEntry& e, uint32_t row_bytes) {
-    if (e.s < 0) return nullptr;
+// Step 3: its slot of the cache, < 0 for none.
+__device__ __forceinline__ long long entry_slot(const PagedAttnArgs& a, const PaEntry& e) {
+    if (e.s < 0) return -1;
     if ((unsigned)e.page >= (unsigned)a.num_pages) {
         record_error(a.err, ERRBIT_BOUNDS);
-        return nullptr;
+        return -1;
     }
-    const int off = e.s - divided(e.s, a.by_page) * a.page_size;
-    return static_cast<const uint8_t*>(a.cache) + ((long long)e.page * a.page_size + off) * (long long)row_bytes;
+    return (long long)e.page * a.page_size + (e.s - divided(e.s, a.by_page) * a.page_size);
 }
 
 // A walk over the CTA's tiles.
@@ -336,18 +344,10 @@ __device__ __forceinline__ void read_factors(const float* m, float (&v)[N]) {
     }
 }
 
-// bf16: hands a pair over once all but the N youngest copy groups of the thread have landed.
-template <int N>
-__device__ __forceinline__ void handed(uint64_t* full, int lane) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full);
-}
-
 template <bool FP4, int NH>
 __global__ void __launch_bounds__(PA_THREADS, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const PagedAttnArgs a) {
+    paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                      const PagedAttnArgs a) {
     using L = Pa<NH>;
     constexpr int GH = L::GH, HB = GH < 8 ? GH : 8, PASSES = GH / HB;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -382,7 +382,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         fence_mbar_init();
     }
     if (warp == 16) {
-        if (lane == 0) tma_prefetch_desc(&qmap);
+        if (lane == 0) {
+            tma_prefetch_desc(&qmap);
+            if (!FP4) tma_prefetch_desc(&kmap);
+        }
         tmem_alloc(tmem_slot, L::TMEM_COLS);
         tmem_relinquish();
     }
@@ -464,7 +467,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (loads > units) mbar_wait(qfull, (loads - 1) & 1, a.err);  // leave no copy in flight
     } else {
         // ---------------------------------------------------------------- rows, softmax and output
-        constexpr uint32_t ROW_BYTES = FP4 ? LI_KV4_ROW_BYTES : PA_D * 2;
         // rows: a thread's half of one chunk of each pair; eight neighbouring threads of a store share a chunk and
         // differ in their swizzled 16-byte unit, so stores meet no bank twice
         const int r = warp * 8 + ((lane >> 1) & 7), hi = lane >> 4, half = lane & 1;
@@ -486,7 +488,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         PaEntry e1, e2;
         uint4 code[FP4 ? 4 : 1];
         uint2 sc = make_uint2(0, 0);                // 4 bits: pair 2 hi + half's eight scales
-        const uint8_t* src = nullptr;               // the row of tile np
+        const uint8_t* src = nullptr;               // the row of tile np (4 bits: its address,
+        int src_row = 0;                            // bf16: its number)
+        bool here = false;                          // it exists
         bool more = false;                          // tile np exists
         uint32_t np = 0;                            // tiles brought in
         bool ok = true;
@@ -500,7 +504,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         };
         auto look_ahead = [&]() {
             more = e1.req >= 0;
-            src = entry_row(a, e1, ROW_BYTES);
+            const long long slot = entry_slot(a, e1);
+            if constexpr (!FP4) {
+                src_row = slot < 0 ? 0x7fffffff : (int)slot;  // (past every end: zeros)
+            } else {
+                src = slot < 0 ? nullptr : static_cast<const uint8_t*>(a.cache) + slot * LI_KV4_ROW_BYTES;
+            }
+            here = slot >= 0;
             if constexpr (FP4) {
                 const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -515,7 +525,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // Brings tile np in, pair by pair as the tile before releases them.
         auto bring = [&]() {
             const uint32_t free_parity = (np & 1) ^ 1;
-            if (hi == 0 && half == 0) vflag[(np & 1) * PA_M + r] = src ? 1 : 0;  // (last read two tiles ago)
+            if (hi == 0 && half == 0) vflag[(np & 1) * PA_M + r] = here ? 1 : 0;  // (last read two tiles ago)
             if constexpr (FP4) {
                 const uint4 z = make_uint4(0, 0, 0, 0);  // (the rotary part is due last: held only from here)
                 const uint4 rot0 = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + (4 * half + 2 * hi) * 16)) : z;
@@ -549,27 +559,19 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[PA_PAIRS - 1]);
             } else {
-                const uint8_t* at = src ? src : static_cast<const uint8_t*>(a.cache);
-                const uint32_t bytes = src ? 16u : 0u;  // 0: the unit is filled with zeros, nothing is read
-                const int off = src ? hi * 128 + half * 64 : 0, step = src ? 256 : 0, unit = src ? 16 : 0;
+                // the warp's eight rows are two gathers of four; lanes 0-8 take the first one's chunks, 9-17 the second's
+                const int group = lane >= 9, chunk = lane - 9 * group;
+                int four[4];
 #pragma unroll
-                for (int p = 0; p < PA_PAIRS - 1; ++p) {
+                for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, src_row, 2 * (4 * group + i));
+                const uint32_t to = smem_u32(ks) + chunk * PA_CHUNK + (warp * 8 + 4 * group) * 128;
+#pragma unroll
+                for (int p = 0; p < PA_PAIRS; ++p) {
                     ok = ok && mbar_wait(&empty[p], free_parity, a.err);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        pa_cp_async16((dst0 ^ (i << 4)) + 2 * p * PA_CHUNK, at + off + p * step + i * unit, bytes);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (lane == 0) mbar_arrive_expect_tx(&full[p], (p < PA_PAIRS - 1 ? 2 : 1) * 8 * 128);
+                    __syncwarp();
+                    if (lane < 18 && chunk >> 1 == p) pa_gather4(to, &kmap, chunk * 64, four, &full[p]);
                 }
-                ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
-                const int roff = src ? 1024 + (4 * half + 2 * hi) * 16 : 0;
-                pa_cp_async16(rdst0, at + roff, bytes);
-                pa_cp_async16(rdst0 ^ 16, at + roff + unit, bytes);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                handed<4>(&full[0], lane);
-                handed<3>(&full[1], lane);
-                handed<2>(&full[2], lane);
-                handed<1>(&full[3], lane);
-                handed<0>(&full[4], lane);
             }
             ++np;
             look_ahead();
@@ -759,7 +761,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             }
             tc_fence_before();  // the next unit's pready hands O on
         }
-        if constexpr (!FP4) asm volatile("cp.async.wait_all;" ::: "memory");
+        // (after a wait that ran out: leave no copy in flight)
+        if (!FP4 && !ok)
+            for (int p = 0; p < PA_PAIRS; ++p) mbar_wait(&full[p], (np & 1) ^ 1, a.err);
     }
     __syncwarp();
     __syncthreads();
@@ -846,7 +850,7 @@ __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedA
 constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <bool FP4, int NH>
-li_status launch_units(const CUtensorMap& qmap, const PagedAttnArgs& a, cudaStream_t st) {
+li_status launch_units(const CUtensorMap& qmap, const CUtensorMap& kmap, const PagedAttnArgs& a, cudaStream_t st) {
     static bool attr_done[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -859,7 +863,7 @@ li_status launch_units(const CUtensorMap& qmap, const PagedAttnArgs& a, cudaStre
         if (dev < 64) attr_done[dev] = true;
     }
     const int grid = a.units < host_num_sms() ? a.units : host_num_sms();
-    if (launch_pdl(paged_attn_kernel<FP4, NH>, dim3(grid), dim3(PA_THREADS), Pa<NH>::SMEM, st, 1, qmap, a) !=
+    if (launch_pdl(paged_attn_kernel<FP4, NH>, dim3(grid), dim3(PA_THREADS), Pa<NH>::SMEM, st, 1, qmap, kmap, a) !=
         cudaSuccess) {
         cudaGetLastError();
         return LI_ERR_CUDA;
@@ -908,7 +912,7 @@ size_t paged_attn_workspace_bytes(int rows, int heads, int splits) {
     return up256(parts * PA_DV * 4) + 2 * up256(parts * 4);
 }
 
-li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, int heads_per_unit, bool fp4, void* workspace,
+li_status launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap, PagedAttnArgs a, int heads_per_unit, bool fp4, void* workspace,
                             cudaStream_t st) {
     a.by_page = divisor_of(a.page_size);
     if (a.splits > 1) {
@@ -920,13 +924,13 @@ li_status launch_paged_attn(const CUtensorMap& qmap, PagedAttnArgs a, int heads_
     }
     li_status s;
     if (fp4)
-        s = heads_per_unit == 64   ? launch_units<true, 64>(qmap, a, st)
-            : heads_per_unit == 32 ? launch_units<true, 32>(qmap, a, st)
-                                   : launch_units<true, 16>(qmap, a, st);
+        s = heads_per_unit == 64   ? launch_units<true, 64>(qmap, kmap, a, st)
+            : heads_per_unit == 32 ? launch_units<true, 32>(qmap, kmap, a, st)
+                                   : launch_units<true, 16>(qmap, kmap, a, st);
     else
-        s = heads_per_unit == 64   ? launch_units<false, 64>(qmap, a, st)
-            : heads_per_unit == 32 ? launch_units<false, 32>(qmap, a, st)
-                                   : launch_units<false, 16>(qmap, a, st);
+        s = heads_per_unit == 64   ? launch_units<false, 64>(qmap, kmap, a, st)
+            : heads_per_unit == 32 ? launch_units<false, 32>(qmap, kmap, a, st)
+                                   : launch_units<false, 16>(qmap, kmap, a, st);
     if (s != LI_OK) return s;
     if (a.splits > 1) {
         const size_t smem = a.splits * sizeof(float);
