@@ -867,7 +867,7 @@ static li_status paged_attention(const void* q, PagedAttnArgs a, const li_attn_d
     if (!(d.scale > 0.f) || !(d.scale < 3.0e38f)) return LI_ERR_INVALID_ARG;
     if (d.cache_dtype != LI_DTYPE_E2M1 && d.cache_dtype != LI_DTYPE_BF16) return LI_ERR_UNSUPPORTED;
     if (d.heads > 4096 || positions > (1 << 28)) return LI_ERR_UNSUPPORTED;
-    if (d.cache_dtype == LI_DTYPE_BF16 && (int64_t)d.num_pages * d.page_size >= (1ll << 31) - 1) return LI_ERR_UNSUPPORTED;
+    if ((int64_t)d.num_pages * d.page_size >= (1ll << 31) - 1) return LI_ERR_UNSUPPORTED;
     if (d.rows == 0) return LI_OK;
     if (!a.req && d.rows > d.requests) return LI_ERR_INVALID_ARG;
     if (!a.table && (int64_t)d.requests * d.max_blocks > d.num_pages) return LI_ERR_INVALID_ARG;
@@ -892,10 +892,11 @@ static li_status paged_attention(const void* q, PagedAttnArgs a, const li_attn_d
     CUtensorMap qmap;
     if (!encode_map_3d_bf16(&qmap, q, 576, d.heads, d.rows, plan.heads)) return LI_ERR_CUDA;
     const bool fp4 = d.cache_dtype == LI_DTYPE_E2M1;
-    CUtensorMap kmap = qmap;  // (4 bits: unused)
-    // (a cache without a page is never read, but the gathers want a map: any memory does)
-    const uint64_t slots = (uint64_t)d.num_pages * d.page_size;
-    if (!fp4 && !encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, slots ? a.cache : q, 576, slots ? slots : 1, 1152, 64, 1))
+    // the cache's rows as bf16 (of a 4-bit row only its rotary part is read that way); a cache without a page is
+    // never read, but the gathers want a map: any memory does
+    const uint64_t slots = (uint64_t)d.num_pages * d.page_size, width = fp4 ? LI_KV4_ROW_BYTES / 2 : 576;
+    CUtensorMap kmap;
+    if (!encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, slots ? a.cache : q, width, slots ? slots : 1, width * 2, 64, 1))
         return LI_ERR_CUDA;
     return launch_paged_attn(qmap, kmap, a, plan.heads, fp4, workspace, stream);
 }

@@ -225,8 +225,8 @@ struct PagedAttnPlan {
 };
 PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms);
 size_t paged_attn_workspace_bytes(int rows, int heads, int splits);
-// qmap: q as [rows, heads, 576] bf16, box 64 x heads_per_unit x 1, 128-byte swizzle; kmap (bf16 cache): its rows of 576,
-// box 64 x 1, 128-byte swizzle
+// qmap: q as [rows, heads, 576] bf16, box 64 x heads_per_unit x 1, 128-byte swizzle; kmap: the cache's rows as bf16 (576 or
+// LI_KV4_ROW_BYTES / 2 elements), box 64 x 1, 128-byte swizzle
 li_status launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap, PagedAttnArgs a, int heads_per_unit, bool fp4,
                             void* workspace, cudaStream_t st);
 

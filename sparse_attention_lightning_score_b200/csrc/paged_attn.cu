@@ -79,7 +79,7 @@ struct Pa {
 static_assert(Pa<64>::SMEM <= 232448, "shared memory per CTA");
 static_assert(Pa<16>::K % 1024 == 0, "the rows' swizzle atoms");
 
-// 64 elements (from x) of four rows of a bf16 cache, 128 bytes each, side by side at dst in the swizzled layout;
+// 64 bf16 elements (from x) of four rows of the cache, 128 bytes each, side by side at dst in the swizzled layout;
 // a row past the end reads as zeros.  The map's box is one row high.
 __device__ __forceinline__ void pa_gather4(uint32_t dst, const void* map, int x, const int (&row)[4], uint64_t* bar) {
     asm volatile(
@@ -98,6 +98,10 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Loads that stay where they are written, far ahead of their use (a plain load is moved down to it: the tile
+// then waits 600 to 1800 cycles for its rows).  Zero where there is no row.
+__device__ __forceinline__ uint4 early16(const uint8_t* p) { return p ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0,0,0,0); }
+__device__ __forceinline__ uint2 early8(const uint8_t* p) { return p ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0,0); }
 // 3-D tiled load (see tma_load_2d).
 __device__ __forceinline__ void pa_tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar,
                                                uint64_t policy) {
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     if (warp == 16) {
         if (lane == 0) {
             tma_prefetch_desc(&qmap);
-            if (!FP4) tma_prefetch_desc(&kmap);
+            tma_prefetch_desc(&kmap);
         }
         tmem_alloc(tmem_slot, L::TMEM_COLS);
         tmem_relinquish();
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         const int r = warp * 8 + ((lane >> 1) & 7), hi = lane >> 4, half = lane & 1;
         // (unit 4 half + i of the row lies at dst0 ^ 16 i: the swizzle is an exclusive or of the unit)
         const uint32_t dst0 = smem_u32(ks) + hi * PA_CHUNK + sw128_offset(r, 4 * half);
-        const uint32_t rdst0 = smem_u32(ks) + (PA_CH - 1) * PA_CHUNK + sw128_offset(r, 4 * half + 2 * hi);
+        const uint32_t rdst = smem_u32(ks) + (PA_CH - 1) * PA_CHUNK + warp * 8 * 128;
         // softmax: GH heads of group g; q4 is the warp's quarter of the TMEM lanes
         const int g = warp >> 2, q4 = warp & 3;
         const int row = q4 * 32 + lane;            // position of the tile; latent element of an O block
@@ -488,8 +492,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         PaEntry e1, e2;
         uint4 code[FP4 ? 4 : 1];
         uint2 sc = make_uint2(0, 0);                // 4 bits: pair 2 hi + half's eight scales
-        const uint8_t* src = nullptr;               // the row of tile np (4 bits: its address,
-        int src_row = 0;                            // bf16: its number)
+        int src = 0;                                // the slot of the thread's row of tile np
         bool here = false;                          // it exists
         bool more = false;                          // tile np exists
         uint32_t np = 0;                            // tiles brought in
@@ -505,18 +508,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         auto look_ahead = [&]() {
             more = e1.req >= 0;
             const long long slot = entry_slot(a, e1);
-            if constexpr (!FP4) {
-                src_row = slot < 0 ? 0x7fffffff : (int)slot;  // (past every end: zeros)
-            } else {
-                src = slot < 0 ? nullptr : static_cast<const uint8_t*>(a.cache) + slot * LI_KV4_ROW_BYTES;
-            }
             here = slot >= 0;
+            src = here ? (int)slot : 0x7fffffff;  // (past every end: a gather fills in zeros)
             if constexpr (FP4) {
-                const uint4 z = make_uint4(0, 0, 0, 0);
+                const uint8_t* from = here ? static_cast<const uint8_t*>(a.cache) + slot * LI_KV4_ROW_BYTES : nullptr;
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    code[p] = src ? __ldg(reinterpret_cast<const uint4*>(src + p * 64 + hi * 32 + half * 16)) : z;
-                sc = src ? __ldg(reinterpret_cast<const uint2*>(src + 256 + (2 * hi + half) * 8)) : make_uint2(0, 0);
+                for (int p = 0; p < 4; ++p) code[p] = early16(from ? from + p * 64 + hi * 32 + half * 16 : nullptr);
+                sc = early8(from ? from + 256 + (2 * hi + half) * 8 : nullptr);
             }
             e1 = e2;
             entry_page(a, e1);
@@ -526,44 +524,54 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         auto bring = [&]() {
             const uint32_t free_parity = (np & 1) ^ 1;
             if (hi == 0 && half == 0) vflag[(np & 1) * PA_M + r] = here ? 1 : 0;  // (last read two tiles ago)
+            // the warp's eight rows make two gathers of four
+            const int group = FP4 ? lane & 1 : lane >= 9;
+            int four[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, src, 2 * (4 * group + i));
             if constexpr (FP4) {
-                const uint4 z = make_uint4(0, 0, 0, 0);  // (the rotary part is due last: held only from here)
-                const uint4 rot0 = src ? __ldg(reinterpret_cast<const uint4*>(src + 288 + (4 * half + 2 * hi) * 16)) : z;
-                const uint4 rot1 = src ? __ldg(reinterpret_cast<const uint4*>(src + 304 + (4 * half + 2 * hi) * 16)) : z;
+                uint32_t sw[4];
 #pragma unroll
                 for (int p = 0; p < PA_PAIRS - 1; ++p) {
-                    // the pair's scales are with the row's p-th thread: hi picks the chunk, half the two blocks
                     const int from = (lane & 14) | (p & 1) | ((p & 2) << 3);
                     const uint32_t w0 = __shfl_sync(0xffffffffu, sc.x, from), w1 = __shfl_sync(0xffffffffu, sc.y, from);
-                    const __half2 s = scales2(((hi ? w1 : w0) >> (16 * half)) & 0xffffu);
+                    sw[p] = hi ? w1 : w0;
+                }
+                uint32_t o[2][4];
+                const __half2 sA = scales2((sw[0] >> (16 * half)) & 0xffffu);
+                expand8(code[0].x, __low2half2(sA), o[0]);
+                expand8(code[0].y, __low2half2(sA), o[1]);
+#pragma unroll
+                for (int p = 0; p < PA_PAIRS - 1; ++p) {
+                    const __half2 s = scales2((sw[p] >> (16 * half)) & 0xffffu);
                     const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
-                    uint32_t o[4];
                     ok = ok && mbar_wait(&empty[p], free_parity, a.err);
                     const uint32_t at = dst0 + 2 * p * PA_CHUNK;
-                    expand8(code[p].x, s0, o);
-                    st_shared16(at, o[0], o[1], o[2], o[3]);
-                    expand8(code[p].y, s0, o);
-                    st_shared16(at ^ 16, o[0], o[1], o[2], o[3]);
-                    expand8(code[p].z, s1, o);
-                    st_shared16(at ^ 32, o[0], o[1], o[2], o[3]);
-                    expand8(code[p].w, s1, o);
-                    st_shared16(at ^ 48, o[0], o[1], o[2], o[3]);
+                    st_shared16(at, o[0][0], o[0][1], o[0][2], o[0][3]);
+                    
+                    st_shared16(at ^ 16, o[1][0], o[1][1], o[1][2], o[1][3]);
+                    expand8(code[p].z, s1, o[0]);
+                    st_shared16(at ^ 32, o[0][0], o[0][1], o[0][2], o[0][3]);
+                    expand8(code[p].w, s1, o[0]);
+                    st_shared16(at ^ 48, o[0][0], o[0][1], o[0][2], o[0][3]);
+                    if (p < PA_PAIRS - 2) {  // the next pair's first words, while the stores drain before the fence
+                        const __half2 sn = scales2((sw[p + 1] >> (16 * half)) & 0xffffu);
+                        expand8(code[p + 1].x, __low2half2(sn), o[0]);
+                        expand8(code[p + 1].y, __low2half2(sn), o[1]);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&full[p]);
+                    if (p == PA_PAIRS - 3) {  // the rotary part (free by now) comes in under the last pair's expansion
+                        ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
+                        if (lane == 0) mbar_arrive_expect_tx(&full[PA_PAIRS - 1], 8 * 128);
+                        __syncwarp();
+                        if (lane < 2)
+                            pa_gather4(rdst + lane * 512, &kmap, (PA_DV / 2 + PA_DV / 16) / 2, four, &full[PA_PAIRS - 1]);
+                    }
                 }
-                ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
-                st_shared16(rdst0, rot0.x, rot0.y, rot0.z, rot0.w);
-                st_shared16(rdst0 ^ 16, rot1.x, rot1.y, rot1.z, rot1.w);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[PA_PAIRS - 1]);
             } else {
-                // the warp's eight rows are two gathers of four; lanes 0-8 take the first one's chunks, 9-17 the second's
-                const int group = lane >= 9, chunk = lane - 9 * group;
-                int four[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, src_row, 2 * (4 * group + i));
+                const int chunk = lane - 9 * group;  // lanes 0-8 take the first one's chunks, 9-17 the second's
                 const uint32_t to = smem_u32(ks) + chunk * PA_CHUNK + (warp * 8 + 4 * group) * 128;
 #pragma unroll
                 for (int p = 0; p < PA_PAIRS; ++p) {
@@ -762,7 +770,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             tc_fence_before();  // the next unit's pready hands O on
         }
         // (after a wait that ran out: leave no copy in flight)
-        if (!FP4 && !ok)
+        if (!ok)
             for (int p = 0; p < PA_PAIRS; ++p) mbar_wait(&full[p], (np & 1) ^ 1, a.err);
     }
     __syncwarp();
