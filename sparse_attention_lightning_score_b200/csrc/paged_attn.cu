@@ -883,11 +883,18 @@ li_status launch_units(const CUtensorMap& qmap, const CUtensorMap& kmap, const P
 
 // How many heads a unit takes and how many CTAs share a token's tiles: the pair with the least estimated time,
 // in microseconds.  Units run in waves of one per SM; a unit costs its tiles and a start and end that grow with
-// its heads (the end writes them), parts cost a merge.  For each number of waves the largest count of splits
-// that fits is tried, lowered as far as the longest share stays the same.
+// its heads (the end writes them); parts cost a merge, and their fp32 sums are written and read once more.  For
+// each number of waves the largest count of splits that fits is tried, lowered as far as the longest share stays
+// the same.  Measured, 4-bit rows, 64 / 32 / 16 heads a unit: a tile 3.06 / 2.42 / 2.37 (bf16 rows 2.83 / 2.33 / 2.15).
+// What the rule decides between, as measured: 1 token x 64 heads, 2048 rows: 16 heads in 16 splits 12.4, 64 heads in
+// 16 splits 15.8; 8 x 128, 2048 rows: 64 in 8 23.0, 32 in 4 24.2, 16 in 2 32.6; 32 x 128, 516 rows: 32 unsplit 22.1, 64
+// in 2 26.1, 64 unsplit 26.7; 74 x 16, 1000 rows: 16 in 2 21.7, unsplit 28.4; 1 x 128, 131071 rows: 64 in 74 70, 32 in 74 101.
 PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms) {
     const int tiles = (positions + PA_M - 1) / PA_M;
-    static const struct { int nh; float tile, unit, part; } kind[3] = {{64, 3.6f, 8.f, 2.0f}, {32, 2.95f, 7.f, 1.0f}, {16, 2.7f, 6.f, 0.5f}};
+    static const struct {
+        int nh;
+        double tile, unit;
+    } kind[3] = {{64, 3.05, 4.2}, {32, 2.4, 3.0}, {16, 2.35, 2.4}};
     PagedAttnPlan best{64, 1};
     double least = 1e30;
     for (const auto& k : kind) {
@@ -904,7 +911,8 @@ PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms) {
                 if (s < 2) continue;
                 w = (base * s + sms - 1) / sms;
             }
-            const double cost = w * (share * k.tile + k.unit + (s > 1 ? k.part : 0.f)) + (s > 1 ? 4.0 + 0.02 * s : 0.0);
+            const double merge = s > 1 ? 3.0 + w + (double)rows * heads * s * (2 * PA_DV * sizeof(float)) / 8e6 : 0.0;
+            const double cost = w * (share * k.tile + k.unit) + merge;
             if (cost < least) {
                 least = cost;
                 best = PagedAttnPlan{k.nh, s};
