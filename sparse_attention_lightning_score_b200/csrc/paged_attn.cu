@@ -58,6 +58,7 @@ constexpr int PA_CHUNK = PA_M * 128;       // 16 KB
 constexpr int PA_WORKERS = 512;            // warps 0-15
 constexpr int PA_THREADS = PA_WORKERS + 32;
 constexpr float PA_RAISE = 8.f;            // log2: a head's maximum is raised when exceeded by more
+constexpr float PA_NOTHING = -3e38f;       // subtracted while a head has met no logit yet: any is more than PA_RAISE above
 
 // What depends on NH, the heads of a unit (MMA N): 64, 32 or 16.
 template <int NH>
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                         tmem_ld(at, s);  // (read again rather than held: registers are short)
                         tmem_ld_wait();
                         __syncwarp();
-                        if (lane < HB) w8[lane] = m_use == -INFINITY ? 0.f : m_use;
+                        if (lane < HB) w8[lane] = m_use == -INFINITY ? PA_NOTHING : m_use;
                         __syncwarp();
                         read_factors(w8, v);
 #pragma unroll
@@ -732,7 +733,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             const bool whole = a.splits == 1;
             const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;  // [row][split][head]
             if (!whole && q4 == 0 && lane < nh) {
-                a.mpart[part + lane] = PASSES == 1 || lane < HB ? m_run[0] : m_run[PASSES - 1];  // (lane % HB is lane's)
+                const float m = PASSES == 1 || lane < HB ? m_run[0] : m_run[PASSES - 1];  // (lane % HB is lane's)
+                // without a maximum the sum is 0 (nothing visible) or NaN, which the merge must not drop
+                a.mpart[part + lane] = m == -INFINITY && sum != 0.f ? 0.f : m;
                 a.lpart[part + lane] = sum;
             }
             if (lane < GH) wm[lane] = sum == 0.f ? 0.f : 1.f / sum;

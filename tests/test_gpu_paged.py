@@ -444,6 +444,40 @@ def test_attention_maximum_that_keeps_rising(kind):
         c.check(out, [np.arange(2000)])
 
 
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+@pytest.mark.parametrize("R,H,k", [(1, 64, 2048), (8, 128, 2048), (40, 256, 512), (20, 16, 1000), (40, 96, 500)])
+def test_attention_holes_before_far_negative_logits(kind, R, H, k):
+    """Every second tile of 128 list entries has nothing, the first among them, and every logit is far below zero:
+    the weights are taken against the logits that are there, whatever the empty tiles left as a maximum."""
+    c = Case(R, 1, H, 3000, 64, kind, seed=R + k, scale=0.3,
+             shape=lambda x: torch.cat([x[:, :512], 20 + 4 * x[:, 512:].abs()], 1))
+    c.q = torch.cat([c.q[:, :, :512] * 0.05, -2 - c.q[:, :, 512:].abs()], 2).to(torch.bfloat16)
+    sel = c.select(k)
+    for a in range(0, k, 256):
+        sel[:, a:a + 128] = -1
+    out = api.li_paged_sparse_attention(c.q.to(DEV), c.cache, torch.from_numpy(sel).to(DEV), c.scale, **c.kw())
+    c.check(out, _lists(sel))
+    assert api.li_get_last_error() == LI_OK
+
+
+@pytest.mark.parametrize("R,H,k", [(1, 64, 2048), (8, 128, 2048), (40, 256, 512)])
+def test_attention_nan_in_a_visible_place_is_passed_on(R, H, k):
+    """Split or whole: a head whose query is NaN gives NaN, and so does every head of a token that selects a NaN row;
+    the others are as they would be."""
+    c = Case(R, 1, H, 3000, 64, "bf16", seed=k)
+    sel = c.select(k)
+    s = int(sel[0, 1])
+    c.cache.view(-1, 576)[int(c.table[0, s // 64]) * 64 + s % 64] = float("nan")
+    q = c.q.to(DEV)
+    q[R - 1, 5] = float("nan")
+    out = api.li_paged_sparse_attention(q, c.cache, torch.from_numpy(sel).to(DEV), c.scale, **c.kw())
+    assert out[0].isnan().all() and out[R - 1, 5].isnan().all()
+    if R > 1:
+        keep = [h for h in range(H) if h != 5]
+        assert not out[1:, keep].isnan().any()
+        c.check(out, _lists(sel), skip=(0, R - 1))
+
+
 def test_attention_masks():
     """Rows with nothing selected, holes and repeats in the list, padding tokens left as they were, NaN and
     infinities in rows that nothing selects."""
