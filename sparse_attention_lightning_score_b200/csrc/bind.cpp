@@ -77,14 +77,30 @@ struct Out {
             ptr = p.take(tensor(given, name), name, t, shape);
             object = Py_NewRef(given);
         } else {
-            at::Tensor x = p.empty(shape, t);
-            ptr = x.data_ptr();
-            object = THPVariable_Wrap(std::move(x));
-            if (!object) throw Raised{};
+            wrap(p.empty(shape, t));
+        }
+    }
+    // ... or a new vector from byte `offset` of an allocation that several outputs share (an allocation costs the host
+    // half a microsecond; a tensor over one that is there, a tenth)
+    Out(const Place& p, PyObject* given, const char* name, at::ScalarType t, int64_t n, at::Tensor& shared, int64_t offset) {
+        if (given != Py_None) {
+            ptr = p.take(tensor(given, name), name, t, {n});
+            object = Py_NewRef(given);
+        } else {
+            at::Tensor x = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(shared.storage()), shared.key_set(),
+                                                                    c10::scalarTypeToTypeMeta(t));
+            x.unsafeGetTensorImpl()->set_storage_offset(offset / (int64_t)c10::elementSize(t));
+            x.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+            wrap(std::move(x));
         }
     }
     Out(const Out&) = delete;
     ~Out() { Py_XDECREF(object); }
+    void wrap(at::Tensor&& x) {
+        ptr = x.data_ptr();
+        object = THPVariable_Wrap(std::move(x));
+        if (!object) throw Raised{};
+    }
     PyObject* give() {
         PyObject* o = object;
         object = nullptr;
@@ -166,8 +182,16 @@ PyObject* block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
         auto* tp = static_cast<int32_t*>(p.take(table, "block_table", I32));
         auto* fp = static_cast<int32_t*>(p.take(pool, "free_pages", I32));
         auto* at0 = static_cast<int32_t*>(p.maybe(v[7], "free_start", I32, {1}));
-        Out slots(p, v[8], "slots", I64, {t}), pos(p, v[9], "positions", I32, {t}), req(p, v[10], "requests", I32, {t}),
-            starts(p, v[11], "starts", I32, {R + 1}), next(p, v[12], "free_next", I32, {1});
+        // new outputs lie one behind the other in one allocation (slots first: 8 bytes each)
+        const int64_t wide = v[8] == Py_None ? 8 * t : 0, one = v[9] == Py_None ? 4 * t : 0, two = v[10] == Py_None ? 4 * t : 0,
+                      ends = v[11] == Py_None ? 4 * (R + 1) : 0, last = v[12] == Py_None ? 4 : 0;
+        const int64_t bytes = wide + one + two + ends + last;
+        at::Tensor shared;
+        if (bytes) shared = p.empty({bytes}, U8);
+        Out slots(p, v[8], "slots", I64, t, shared, 0), pos(p, v[9], "positions", I32, t, shared, wide),
+            req(p, v[10], "requests", I32, t, shared, wide + one),
+            starts(p, v[11], "starts", I32, R + 1, shared, wide + one + two),
+            next(p, v[12], "free_next", I32, 1, shared, wide + one + two + ends);
         check("li_block_tables",
               li_block_tables(sp, np, size_of(R, "requests"), tp, size_of(table.size(1), "max_blocks"), page, pages, fp,
                               size_of(pool.numel(), "free_pages"), at0, tokens, static_cast<int64_t*>(slots.ptr),
