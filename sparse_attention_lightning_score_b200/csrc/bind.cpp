@@ -183,8 +183,9 @@ PyObject* block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
         auto* fp = static_cast<int32_t*>(p.take(pool, "free_pages", I32));
         auto* at0 = static_cast<int32_t*>(p.maybe(v[7], "free_start", I32, {1}));
         // new outputs lie one behind the other in one allocation (slots first: 8 bytes each)
-        const int64_t wide = v[8] == Py_None ? 8 * t : 0, one = v[9] == Py_None ? 4 * t : 0, two = v[10] == Py_None ? 4 * t : 0,
-                      ends = v[11] == Py_None ? 4 * (R + 1) : 0, last = v[12] == Py_None ? 4 : 0;
+        const int64_t wide = v[8] == Py_None ? 8 * t : 0, one = v[9] == Py_None ? 4 * t : 0;
+        const int64_t two = v[10] == Py_None ? 4 * t : 0, ends = v[11] == Py_None ? 4 * (R + 1) : 0;
+        const int64_t last = v[12] == Py_None ? 4 : 0;
         const int64_t bytes = wide + one + two + ends + last;
         at::Tensor shared;
         if (bytes) shared = p.empty({bytes}, U8);

@@ -896,7 +896,8 @@ static li_status paged_attention(const void* q, PagedAttnArgs a, const li_attn_d
     // never read, but the gathers want a map: any memory does
     const uint64_t slots = (uint64_t)d.num_pages * d.page_size, width = fp4 ? LI_KV4_ROW_BYTES / 2 : 576;
     CUtensorMap kmap;
-    if (!encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, slots ? a.cache : q, width, slots ? slots : 1, width * 2, 64, 1))
+    if (!encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, slots ? a.cache : q, width, slots ? slots : 1, width * 2,
+                       64, 1))
         return LI_ERR_CUDA;
     return launch_paged_attn(qmap, kmap, a, plan.heads, fp4, workspace, stream);
 }

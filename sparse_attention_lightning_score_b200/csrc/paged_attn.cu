@@ -9,36 +9,40 @@
 // has 6 significant bits, so a 4-bit row is expanded to bf16 exactly and the
 // two formats share everything behind the producer warps.
 //
-// One CTA (one per SM, persistent) takes units of one token, 64 heads and a
-// share of the token's visible positions, 128 positions (a tile) at a time.
+// One CTA (one per SM, persistent) takes units of one token, 64, 32 or 16 heads and
+// a share of the token's visible positions, 128 positions (a tile) at a time.
 // Sixteen warps do all that is not a matrix product, in turn: they bring a tile's
 // rows into shared memory, and when its scores are done they make its weights.
 //   - Rows: each tile's rows lie once in shared memory, as bf16 in nine 16 KB chunks
-//     of 64 elements x 128 positions (128-byte swizzle), handed over in pairs.  A row
-//     belongs to four threads.  4 bits: a thread has its quarter of the row in
-//     registers one whole tile ahead (and the row's page and position one and two
-//     tiles ahead), and expands it pair by pair; bf16: the copy engine gathers four
-//     rows of a chunk at a time (16-byte cp.async by the threads kept the
-//     load-store unit busy for 4000 cycles a tile).
-//   - Weights: one position per TMEM lane, 16 heads per group of four warps.  The
-//     running maximum of a head is raised only when a tile exceeds it by more than
-//     2^8 (p stays below 2^8, which bf16 and the fp32 sums hold as exactly as
-//     p <= 1), so after a unit's first tile no maximum is exchanged and O is
+//     of 64 elements x 128 positions (128-byte swizzle), handed over in pairs.
+//     bf16 rows and the rotary part of 4-bit rows come by gathers of the copy engine,
+//     four rows of a chunk each (16-byte cp.async by the threads kept the load-store
+//     unit busy for 4000 cycles a tile: the window below took 385 us).  The 4-bit
+//     codes of a row belong to four threads: each holds its quarter in registers a
+//     whole tile ahead (the row's page two and its position three tiles ahead, one
+//     dependent load each) and expands it pair by pair.
+//   - Weights: one position per TMEM lane, a quarter of the heads per group of four
+//     warps.  The running maximum of a head is raised only when a tile exceeds it by
+//     more than 2^8 (p stays below 2^8, which bf16 and the fp32 sums hold as exactly
+//     as p <= 1), so after a unit's first tile no maximum is exchanged and O is
 //     rescaled in TMEM almost never.  Sums are fp32; p is rounded to bf16 for the
-//     product (2^-9 each, the same step as the bf16 output).
-//   - Warp 16 issues S^T = K Q^T (M = 128 positions, N = 64 heads, K = 576) and
-//     O^T += V^T P^T (M = 128 latent elements, four blocks, N = 64, K = 128), both
+//     product (2^-9 to 2^-8 of it, the same step as the bf16 output's).
+//   - Warp 16 issues S^T = K Q^T (M = 128 positions, N = the unit's heads, K = 576) and
+//     O^T += V^T P^T (M = 128 latent elements, four blocks, K = 128), both
 //     from the same chunks: K is read K-major, V^T MN-major, so nothing is loaded
 //     or transposed a second time.  P takes the rotary chunk's place, which V does
 //     not need and whose scores are done by then.
 // A pair is released as soon as its value product is done, so the next tile's rows
-// come in under this tile's value product.  What bounds it: at N = 64 a product
-// reads 6 KB of shared memory per 48 cycles, all that an SM has (measured: 48
-// cycles at N = 64, 64 at N = 128, where TMEM has no room for O), so the 68
-// products of a tile take 3264 cycles and everything else that touches shared
-// memory competes with them.
+// come in under this tile's value product.
+// What bounds it is the chain of a tile, since a tile's rows fill shared memory: its
+// 68 products take 48 cycles each at 64 heads (40 at 32 or 16; at 128 heads 64, but
+// TMEM has no room for their O), the weights between them about 1000, and the rows
+// of a pair (540 to 700 cycles to expand, about 1000 to gather) are hidden only
+// under the value products of the pairs behind it.  Measured: 3.06 us a tile of 64
+// heads in 4 bits (128 heads over a window of 131071: 69.5 us, 0.53 PFLOP/s), 2.83
+// in bf16 (1024 tokens x 128 heads, window 512: 292 us, 0.52 PFLOP/s).
 // With few units the visible tiles are split over several CTAs; a second kernel
-// merges the parts (see paged_attn_splits for the rule).
+// merges the parts (see paged_attn_plan for the rule).
 #include <cuda_fp16.h>
 
 #include "li_common.cuh"
@@ -58,7 +62,7 @@ constexpr int PA_CHUNK = PA_M * 128;       // 16 KB
 constexpr int PA_WORKERS = 512;            // warps 0-15
 constexpr int PA_THREADS = PA_WORKERS + 32;
 constexpr float PA_RAISE = 8.f;            // log2: a head's maximum is raised when exceeded by more
-constexpr float PA_NOTHING = -3e38f;       // subtracted while a head has met no logit yet: any is more than PA_RAISE above
+constexpr float PA_NOTHING = -3e38f;       // the reference of a head without a logit yet: any is more than PA_RAISE above
 
 // What depends on NH, the heads of a unit (MMA N): 64, 32 or 16.
 template <int NH>
@@ -99,10 +103,14 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Loads that stay where they are written, far ahead of their use (a plain load is moved down to it: the tile
-// then waits 600 to 1800 cycles for its rows).  Zero where there is no row.
-__device__ __forceinline__ uint4 early16(const uint8_t* p) { return p ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0,0,0,0); }
-__device__ __forceinline__ uint2 early8(const uint8_t* p) { return p ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0,0); }
+// A thread's part of a row, read a tile ahead of its use.  Zeros where there is no row.
+__device__ __forceinline__ uint4 early16(const uint8_t* p) {
+    return p ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ uint2 early8(const uint8_t* p) {
+    return p ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+}
+
 // 3-D tiled load (see tma_load_2d).
 __device__ __forceinline__ void pa_tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar,
                                                uint64_t policy) {
@@ -120,7 +128,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
                  : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(taddr)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(taddr)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
@@ -129,17 +138,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -432,6 +439,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             const int tiles = w.x.t1 - w.x.t0;
             for (int t = 0; ok && t < tiles; ++t, ++n) {
                 const uint32_t par = n & 1;
+                // The last tile's value product ends with the 16 positions that hold the list's last entry, and bf16
+                // rows behind them are not fetched (window 512 after 16 first positions, 1024 x 128 heads: 299 ->
+                // 292 us; the same skip in the expansion of 4-bit rows cost registers: 69.4 -> 72.5 us over 131071).
+                const int steps = (min(w.x.n - (w.x.t0 + t) * PA_M, PA_M) + 15) / 16;
 #pragma unroll
                 for (int p = 0; p < PA_PAIRS; ++p) {
                     ok = ok && mbar_wait(&full[p], par, a.err);
@@ -439,7 +450,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < (p < PA_PAIRS - 1 ? 8 : 4); ++kk)
                             mma_bf16(tmem_base, k_desc + (2 * p + kk / 4) * (PA_CHUNK >> 4) + (kk & 3) * 2,
-                                     q_desc + (2 * p + kk / 4) * (L::QCHUNK >> 4) + (kk & 3) * 2, IDESC_S, (p | kk) != 0);
+                                     q_desc + (2 * p + kk / 4) * (L::QCHUNK >> 4) + (kk & 3) * 2, IDESC_S,
+                                     (p | kk) != 0);
                     }
                 }
                 if (!ok) break;
@@ -451,7 +463,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     for (int blk = 0; blk < PA_VCH / 2; ++blk) {
 #pragma unroll
                         for (int s = 0; s < PA_M / 16; ++s)
-                            mma_bf16(tmem_base + (uint32_t)(L::O_COL + blk * NH),
+                            if (s < steps) mma_bf16(tmem_base + (uint32_t)(L::O_COL + blk * NH),
                                      v_desc + (2 * blk * PA_CHUNK + s * 2048) / 16, p_desc + s * 2048 / 16, IDESC_O,
                                      (t | s) != 0);
                         tc_commit(&empty[blk]);
@@ -490,7 +502,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // Lookups run ahead of the rows, one dependent load a tile, under the score products: behind tile np the
         // thread's part of tile np + 1 is read (4 bits), the page of np + 2 and the position of np + 3.
         PaWalk w;
-        PaEntry e1, e2;
+        w.start(a);
+        PaEntry e1{-1, -1, -1}, e2{-1, -1, -1};
         uint4 code[FP4 ? 4 : 1];
         uint2 sc = make_uint2(0, 0);                // 4 bits: pair 2 hi + half's eight scales
         int src = 0;                                // the slot of the thread's row of tile np
@@ -503,6 +516,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             e.req = w.more ? 0 : -1;                // (-1: no such tile)
             if (w.more) {
                 entry_position(a, w.x, w.t * PA_M + r, e);
+                if (!FP4 && w.t * PA_M + (warp & ~1) * 8 >= w.x.n) e.s = -2;  // it ends before two warps' 16 rows
                 w.next(a);
             }
         };
@@ -510,7 +524,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             more = e1.req >= 0;
             const long long slot = entry_slot(a, e1);
             here = slot >= 0;
-            src = here ? (int)slot : 0x7fffffff;  // (past every end: a gather fills in zeros)
+            src = here ? (int)slot : !FP4 && e1.s == -2 ? -1 : 0x7fffffff;  // (past every end: a gather fills in zeros)
             if constexpr (FP4) {
                 const uint8_t* from = here ? static_cast<const uint8_t*>(a.cache) + slot * LI_KV4_ROW_BYTES : nullptr;
 #pragma unroll
@@ -525,6 +539,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         auto bring = [&]() {
             const uint32_t free_parity = (np & 1) ^ 1;
             if (hi == 0 && half == 0) vflag[(np & 1) * PA_M + r] = here ? 1 : 0;  // (last read two tiles ago)
+            if (!FP4 && src == -1) {  // (the whole warp) the value product ends before these rows: they stay as they are
+                __syncwarp();
+                if (lane == 0)
+                    for (int p = 0; p < PA_PAIRS; ++p) mbar_arrive(&full[p]);
+                ++np;
+                look_ahead();
+                return;
+            }
             // the warp's eight rows make two gathers of four
             const int group = FP4 ? lane & 1 : lane >= 9;
             int four[4];
@@ -549,7 +571,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     ok = ok && mbar_wait(&empty[p], free_parity, a.err);
                     const uint32_t at = dst0 + 2 * p * PA_CHUNK;
                     st_shared16(at, o[0][0], o[0][1], o[0][2], o[0][3]);
-                    
                     st_shared16(at ^ 16, o[1][0], o[1][1], o[1][2], o[1][3]);
                     expand8(code[p].z, s1, o[0]);
                     st_shared16(at ^ 32, o[0][0], o[0][1], o[0][2], o[0][3]);
@@ -567,8 +588,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                         ok = ok && mbar_wait(&empty[PA_PAIRS - 1], free_parity, a.err);
                         if (lane == 0) mbar_arrive_expect_tx(&full[PA_PAIRS - 1], 8 * 128);
                         __syncwarp();
-                        if (lane < 2)
-                            pa_gather4(rdst + lane * 512, &kmap, (PA_DV / 2 + PA_DV / 16) / 2, four, &full[PA_PAIRS - 1]);
+                        if (lane < 2)  // (it lies behind the codes and scales)
+                            pa_gather4(rdst + lane * 512, &kmap, (PA_DV / 2 + PA_DV / 16) / 2, four,
+                                       &full[PA_PAIRS - 1]);
                     }
                 }
             } else {
@@ -585,7 +607,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             ++np;
             look_ahead();
         };
-        w.start(a);
         if (w.more) {
             position(e1);
             entry_page(a, e1);
@@ -631,9 +652,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 tc_fence_after();
                 const bool valid = vflag[(n & 1) * PA_M + row] != 0;
 #pragma unroll
-                for (int ps8 = 0; ps8 < PASSES; ++ps8) {  // HB heads at a time: registers are short
-                    const uint32_t at = s_at + ps8 * HB;
-                    float* w8 = wm + ps8 * HB;
+                for (int pass = 0; pass < PASSES; ++pass) {  // HB heads at a time: registers are short
+                    const uint32_t at = s_at + pass * HB;
+                    float* w8 = wm + pass * HB;
                     uint32_t s[HB];
                     bool high = t == 0;  // no maximum yet
                     if (!high) {
@@ -657,23 +678,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < HB; ++i) v[i] = valid ? __uint_as_float(s[i]) * c2 : -INFINITY;
                         warp_reduce_scatter<true>(v, lane);
-                        float* r8 = gred + ps8 * 4 * HB;
+                        float* r8 = gred + pass * 4 * HB;
                         if (lane < HB) r8[q4 * HB + lane] = v[0];
                         group_sync(bar);
                         const int k = lane % HB;
                         const float mx = fmaxf(fmaxf(r8[k], r8[HB + k]), fmaxf(r8[2 * HB + k], r8[3 * HB + k]));
-                        const bool raise = mx > m_run[ps8] + PA_RAISE;
-                        const float m_use = raise ? mx : m_run[ps8];
-                        const float f = raise && m_run[ps8] != -INFINITY ? pa_ex2(m_run[ps8] - m_use) : 1.f;
+                        const bool raise = mx > m_run[pass] + PA_RAISE;
+                        const float m_use = raise ? mx : m_run[pass];
+                        const float f = raise && m_run[pass] != -INFINITY ? pa_ex2(m_run[pass] - m_use) : 1.f;
                         const bool rescale = __any_sync(0xffffffffu, f != 1.f);  // the same in the group's four warps
-                        m_run[ps8] = m_use;
+                        m_run[pass] = m_use;
                         if (rescale) {  // O of the tiles before is complete: its commit came before sdone's
                             __syncwarp();
                             if (lane < HB) w8[lane] = f;
                             __syncwarp();
                             read_factors(w8, v);
 #pragma unroll
-                            for (int i = 0; i < HB; ++i) l[ps8 * HB + i] *= v[i];
+                            for (int i = 0; i < HB; ++i) l[pass * HB + i] *= v[i];
 #pragma unroll 1
                             for (int blk = 0; blk < PA_DV / 128; ++blk) {
                                 const uint32_t o_at = at + (uint32_t)(L::O_COL + blk * NH);
@@ -702,16 +723,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     uint32_t pk[HB / 2];
 #pragma unroll
                     for (int j = 0; j < HB / 2; ++j) {
-                        __nv_bfloat162 pp = __floats2bfloat162_rn(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                        __nv_bfloat162 pp =
+                            __floats2bfloat162_rn(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                         pk[j] = *reinterpret_cast<uint32_t*>(&pp);
                     }
                     if constexpr (HB == 8)
-                        *reinterpret_cast<uint4*>(ps + sw128_offset(row, PASSES * g + ps8)) =
+                        *reinterpret_cast<uint4*>(ps + sw128_offset(row, PASSES * g + pass)) =
                             make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     else
-                        *reinterpret_cast<uint2*>(ps + sw128_offset(row, g >> 1) + 8 * (g & 1)) = make_uint2(pk[0], pk[1]);
+                        *reinterpret_cast<uint2*>(ps + sw128_offset(row, g >> 1) + 8 * (g & 1)) =
+                            make_uint2(pk[0], pk[1]);
 #pragma unroll
-                    for (int i = 0; i < HB; ++i) l[ps8 * HB + i] += __uint_as_float(s[i]);
+                    for (int i = 0; i < HB; ++i) l[pass * HB + i] += __uint_as_float(s[i]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -787,9 +810,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 // Merge of a token's splits: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M the
 // largest m_s (maxima are in the log2 domain).  A CTA takes 512 / ST latent elements of one (head, token), four
 // to a thread, the parts dealt over its ST stripes of threads, eight in flight in each; the weights are made once in
-// shared memory.  Latency bound: an L2 read of the maxima, then the parts.  ST = 1 keeps the CTAs few (148 tokens
-// of 64 heads in 2 parts: 66 us a call against 89 with ST = 4), ST = 4 shortens the walk over many parts (74 parts
-// of 128 heads: 77 us a call against 94).
+// shared memory.  Latency bound: an L2 read of the maxima, then the parts.  ST = 1 keeps the CTAs few (a whole call
+// of 24 tokens x 128 heads in 3 parts: 25.4 us, 32.1 with ST = 4; 8 x 128 in 8: 21.8 and 22.6), ST = 4 shortens the walk
+// over more than eight parts (1 x 64 in 16 parts: 12.2 us, 13.2 with ST = 1; 1 x 128 in 74: 66.7 and 82.2).
 constexpr int PA_MERGE = 128;
 template <int ST>
 __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedAttnArgs a) {
@@ -888,10 +911,11 @@ li_status launch_units(const CUtensorMap& qmap, const CUtensorMap& kmap, const P
 // in microseconds.  Units run in waves of one per SM; a unit costs its tiles and a start and end that grow with
 // its heads (the end writes them); parts cost a merge, and their fp32 sums are written and read once more.  For
 // each number of waves the largest count of splits that fits is tried, lowered as far as the longest share stays
-// the same.  Measured, 4-bit rows, 64 / 32 / 16 heads a unit: a tile 3.06 / 2.42 / 2.37 (bf16 rows 2.83 / 2.33 / 2.15).
-// What the rule decides between, as measured: 1 token x 64 heads, 2048 rows: 16 heads in 16 splits 12.4, 64 heads in
-// 16 splits 15.8; 8 x 128, 2048 rows: 64 in 8 23.0, 32 in 4 24.2, 16 in 2 32.6; 32 x 128, 516 rows: 32 unsplit 22.1, 64
-// in 2 26.1, 64 unsplit 26.7; 74 x 16, 1000 rows: 16 in 2 21.7, unsplit 28.4; 1 x 128, 131071 rows: 64 in 74 70, 32 in 74 101.
+// the same.  Measured, 4-bit rows, 64 / 32 / 16 heads a unit: a tile 3.06 / 2.42 / 2.37 (bf16 rows 2.83 / 2.33 /
+// 2.15).  What the rule decides between, as measured: 1 token x 64 heads, 2048 rows: 16 heads in 16 splits 12.4, 64
+// heads in 16 splits 15.8; 8 x 128, 2048 rows: 64 in 8 23.0, 32 in 4 24.2, 16 in 2 32.6; 32 x 128, 516 rows: 32 unsplit
+// 22.1, 64 in 2 26.1, 64 unsplit 26.7; 74 x 16, 1000 rows: 16 in 2 21.7, unsplit 28.4; 1 x 128, 131071 rows: 64 in 74
+// 70, 32 in 74 101.
 PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms) {
     const int tiles = (positions + PA_M - 1) / PA_M;
     static const struct {
@@ -931,8 +955,8 @@ size_t paged_attn_workspace_bytes(int rows, int heads, int splits) {
     return up256(parts * PA_DV * 4) + 2 * up256(parts * 4);
 }
 
-li_status launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap, PagedAttnArgs a, int heads_per_unit, bool fp4, void* workspace,
-                            cudaStream_t st) {
+li_status launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap, PagedAttnArgs a, int heads_per_unit,
+                            bool fp4, void* workspace, cudaStream_t st) {
     a.by_page = divisor_of(a.page_size);
     if (a.splits > 1) {
         const size_t parts = (size_t)a.rows * a.splits * a.heads;
@@ -953,9 +977,10 @@ li_status launch_paged_attn(const CUtensorMap& qmap, const CUtensorMap& kmap, Pa
     if (s != LI_OK) return s;
     if (a.splits > 1) {
         const size_t smem = a.splits * sizeof(float);
+        const dim3 block(PA_MERGE);
         const cudaError_t e =
-            a.splits > 8 ? launch_pdl(paged_attn_merge_kernel<4>, dim3(a.heads, 4, a.rows), dim3(PA_MERGE), smem, st, 1, a)
-                          : launch_pdl(paged_attn_merge_kernel<1>, dim3(a.heads, 1, a.rows), dim3(PA_MERGE), smem, st, 1, a);
+            a.splits > 8 ? launch_pdl(paged_attn_merge_kernel<4>, dim3(a.heads, 4, a.rows), block, smem, st, 1, a)
+                         : launch_pdl(paged_attn_merge_kernel<1>, dim3(a.heads, 1, a.rows), block, smem, st, 1, a);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return LI_ERR_CUDA;

@@ -29,7 +29,9 @@ struct BtSum {
 __device__ __forceinline__ BtSum bt_add(BtSum a, BtSum b) { return {a.tokens + b.tokens, a.pages + b.pages}; }
 
 // Pages of n positions.
-__device__ __forceinline__ int bt_pages(const BlockTableArgs& a, int n) { return n > 0 ? divided(n - 1, a.by_page) + 1 : 0; }
+__device__ __forceinline__ int bt_pages(const BlockTableArgs& a, int n) {
+    return n > 0 ? divided(n - 1, a.by_page) + 1 : 0;
+}
 
 // Last index i in [0, n) with v[i] <= x (v ascending, v[0] <= x).
 __device__ __forceinline__ int bt_find(const int32_t* v, int n, int x) {
@@ -125,7 +127,8 @@ __global__ void __launch_bounds__(BT_THREADS) block_table_kernel(const BlockTabl
         }
         return page;
     };
-    for (int t = gid; t < a.max_tokens; t += step) {
+    for (long long i = gid; i < a.max_tokens; i += step) {
+        const int t = (int)i;
         int64_t slot = -1;
         int pos = -1, owner = -1;
         if (t < total) {
@@ -170,8 +173,7 @@ __global__ void __launch_bounds__(BT_THREADS) block_table_kernel(const BlockTabl
 // Many tokens out of place, where most of the bytes are only moved: the copy engine moves
 // them.  A persistent CTA brings a token's heads into a ring of stages by bulk copies, turns
 // the rotated part where it lies, and sends the stage to its place.  HBM bound: each element
-// read once and written once (8192 tokens of 65 heads x 128: the threads' own loads and
-// stores took 68 us).
+// read once and written once (8192 tokens of 64 heads x 128: 43 us, 6.2 TB/s).
 constexpr int RP_THREADS = 256;
 constexpr int RP_UNROLL = 4;
 constexpr int RP_BLOCK = 16;       // most tokens of a CTA
@@ -179,7 +181,9 @@ constexpr int RP_PAIRS = 1024;     // most angles of a CTA
 constexpr int RP_ANGLES = 256;     // most angles of a share of several tokens
 constexpr int RP_STAGES = 3;       // (3 stages and 4 CTAs an SM: 43 us for 8192 x 64 x 128, 4 and 3: 47)
 constexpr int RP_STAGE = 16384;    // bytes of a stage
-constexpr long long RP_BULK = 8 << 20;  // bytes of a call from which it goes by bulk copies
+// Bytes of a call from which it goes by bulk copies (by the threads' own loads: 2.1 MB 3.6 us against 3.0, 8.4 MB 6.1
+// against 4.6, 134 MB 51 against 43; 1 MB 2.6 against 2.9).
+constexpr long long RP_BULK = 2 << 20;
 
 // (written out, so that every form of the call rounds alike)
 __device__ __forceinline__ void rope_pair(float& x, float& y, float c, float s) {
@@ -209,7 +213,8 @@ __device__ __forceinline__ uint4 rope_inside(uint4 v, bool bf16, const float2* c
         }
     } else {
         const float4 a = *reinterpret_cast<const float4*>(cs);
-        float x0 = __uint_as_float(w[0]), y0 = __uint_as_float(w[1]), x1 = __uint_as_float(w[2]), y1 = __uint_as_float(w[3]);
+        float x0 = __uint_as_float(w[0]), y0 = __uint_as_float(w[1]);
+        float x1 = __uint_as_float(w[2]), y1 = __uint_as_float(w[3]);
         rope_pair(x0, y0, a.x, a.y);
         rope_pair(x1, y1, a.z, a.w);
         w[0] = __float_as_uint(x0);
@@ -288,7 +293,8 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& a, const RopePart& c
 }
 
 template <bool BF16, bool HALF>
-__device__ __forceinline__ void rope_rows(const RopeArgs& a, const RopeTensor& t, const RopePart& c, float2* cs, int* live) {
+__device__ __forceinline__ void rope_rows(const RopeArgs& a, const RopeTensor& t, const RopePart& c, float2* cs,
+                                          int* live) {
     constexpr int V = BF16 ? 8 : 4, SIZE = 16 / V;
     const int step = RP_THREADS / t.per_head;          // rows of a pass
     const int slot = threadIdx.x / t.per_head, i = threadIdx.x - slot * t.per_head;
@@ -353,7 +359,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_wide_kernel(const __grid_cons
 // the store of the share that had the stage before has been read out.
 __global__ void __launch_bounds__(RP_THREADS) rope_bulk_kernel(const __grid_constant__ RopeArgs a, const int shares,
                                                               const int angles_max, const DevErr err) {
-    extern __shared__ __align__(128) uint8_t stages[];             // [RP_STAGES][RP_STAGE], then the angles [2][angles_max]
+    extern __shared__ __align__(128) uint8_t stages[];  // [RP_STAGES][RP_STAGE], then the angles [2][angles_max]
     __shared__ uint64_t full[RP_STAGES];
     float2* cs = reinterpret_cast<float2*>(stages + RP_STAGES * RP_STAGE);
     const int n = a.rot_dim / 2, tid = threadIdx.x;
@@ -538,8 +544,8 @@ __device__ __forceinline__ void kv4_block(const uint32_t (&w)[8], uint2& code, u
     code = make_uint2(c[0], c[1]);
 }
 
-// ROWS rows a warp, their loads all in flight: 4 once there are enough of them to fill the GPU (a 65537-row write
-// takes 1 row a warp 22.9 us), else 1 (a short chain).
+// ROWS rows a warp, their loads all in flight: 2 once there are enough of them to fill the GPU, else 1 (a short chain).
+// Rows are read past the caches (__ldcs): nothing reads them again.
 template <bool WIDE, int ROWS>
 __global__ void __launch_bounds__(K4_THREADS) kv4_write_kernel(const Kv4Args a) {
     const int lane = threadIdx.x & 31;
@@ -554,8 +560,8 @@ __global__ void __launch_bounds__(K4_THREADS) kv4_write_kernel(const Kv4Args a) 
         if (i0 + k >= a.n) continue;
         const uint16_t* src = a.rows + (i0 + k) * a.row_stride;
         if constexpr (WIDE) {
-            const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src + lane * 16));
-            const uint4 hi = __ldg(reinterpret_cast<const uint4*>(src + lane * 16) + 1);
+            const uint4 lo = __ldcs(reinterpret_cast<const uint4*>(src + lane * 16));
+            const uint4 hi = __ldcs(reinterpret_cast<const uint4*>(src + lane * 16) + 1);
             w[k][0] = lo.x; w[k][1] = lo.y; w[k][2] = lo.z; w[k][3] = lo.w;
             w[k][4] = hi.x; w[k][5] = hi.y; w[k][6] = hi.z; w[k][7] = hi.w;
             rot[k] = __ldg(reinterpret_cast<const uint32_t*>(src + 512 + lane * 2));
@@ -583,56 +589,47 @@ __global__ void __launch_bounds__(K4_THREADS) kv4_write_kernel(const Kv4Args a) 
     }
 }
 
-// e2m1 x e4m3 has 6 significant bits, so the bf16 row is exact.  A slot < 0 reads as zeros.
-template <int ROWS>
+// e2m1 x e4m3 has 6 significant bits, so the bf16 row is exact.  A slot < 0 reads as zeros.  (65537 rows 19 us, 5.4 TB/s;
+// four rows a warp: the same, and 32768 rows 10.8 against 9.3.)
 __global__ void __launch_bounds__(K4_THREADS) kv4_read_kernel(const Kv4Args a) {
     const int lane = threadIdx.x & 31;
-    const long long i0 = ((long long)blockIdx.x * (K4_THREADS / 32) + (threadIdx.x >> 5)) * ROWS;
+    const long long i = (long long)blockIdx.x * (K4_THREADS / 32) + (threadIdx.x >> 5);
     pdl_wait();
-    long long slot[ROWS];
-    uint2 code[ROWS];
-    uint32_t sbyte[ROWS], rot[ROWS];
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) slot[k] = i0 + k < a.n ? __ldg(a.slots + i0 + k) : -1;
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-        code[k] = make_uint2(0, 0);
-        sbyte[k] = rot[k] = 0;
-        if (slot[k] >= a.num_slots) {
-            if (lane == 0) record_error(a.err, ERRBIT_BOUNDS);
-        } else if (slot[k] >= 0) {
-            const uint8_t* src = a.cache + slot[k] * LI_KV4_ROW_BYTES;
-            code[k] = *reinterpret_cast<const uint2*>(src + lane * 8);
-            sbyte[k] = src[256 + lane];
-            rot[k] = *reinterpret_cast<const uint32_t*>(src + 288 + lane * 4);
-        }
+    if (i >= a.n) return;
+    const long long slot = __ldg(a.slots + i);
+    uint2 code = make_uint2(0, 0);
+    uint32_t sbyte = 0, rot = 0;
+    if (slot >= a.num_slots) {
+        if (lane == 0) record_error(a.err, ERRBIT_BOUNDS);
+    } else if (slot >= 0) {
+        const uint8_t* src = a.cache + slot * LI_KV4_ROW_BYTES;
+        code = *reinterpret_cast<const uint2*>(src + lane * 8);
+        sbyte = src[256 + lane];
+        rot = *reinterpret_cast<const uint32_t*>(src + 288 + lane * 4);
     }
+    uint32_t sh;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"((unsigned short)sbyte));
+    const __half2 s2 = __low2half2(*reinterpret_cast<__half2*>(&sh));
+    uint32_t o[8];
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-        if (i0 + k >= a.n) continue;
-        uint32_t sh;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"((unsigned short)sbyte[k]));
-        const __half2 s2 = __low2half2(*reinterpret_cast<__half2*>(&sh));
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t byte = ((j < 4 ? code[k].x : code[k].y) >> (8 * (j & 3))) & 0xffu;
-            uint32_t h;
-            asm("{\n\t.reg .b8 b, z0, z1, z2;\n\tmov.b32 {b, z0, z1, z2}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-                : "=r"(h)
-                : "r"(byte));
-            // at most 6 x 448 and at least 2^-10: exact in fp16 too
-            const float2 f = __half22float2(__hmul2(*reinterpret_cast<__half2*>(&h), s2));
-            o[j] = bf_pack(f.x, f.y);
-        }
-        uint16_t* dst = a.out + (i0 + k) * 576;
-        *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-        *(reinterpret_cast<uint4*>(dst + lane * 16) + 1) = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint32_t*>(dst + 512 + lane * 2) = rot[k];
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t byte = ((j < 4 ? code.x : code.y) >> (8 * (j & 3))) & 0xffu;
+        uint32_t h;
+        asm("{\n\t.reg .b8 b, z0, z1, z2;\n\tmov.b32 {b, z0, z1, z2}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+            : "=r"(h)
+            : "r"(byte));
+        // at most 6 x 448 and at least 2^-10: exact in fp16 too
+        const float2 f = __half22float2(__hmul2(*reinterpret_cast<__half2*>(&h), s2));
+        o[j] = bf_pack(f.x, f.y);
     }
+    uint16_t* dst = a.out + i * 576;
+    *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    *(reinterpret_cast<uint4*>(dst + lane * 16) + 1) = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint32_t*>(dst + 512 + lane * 2) = rot;
 }
 
-// From this many rows on a warp takes four.
+// From this many rows on a warp takes two (1, 2 and 4 rows a warp: 8192 rows 3.7, 4.2 and 4.4 us, 16384 5.9, 5.9 and
+// 6.8, 65537 21.2, 19.4 and 20.2, 131072 42.1, 36.7 and 37.6: 5.6 TB/s).
 constexpr long long K4_MANY = 16384;
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -720,8 +717,8 @@ li_status launch_rope(RopeArgs a, cudaStream_t st) {
         const long long most = (long long)(227 * 1024 / (smem + 1536)) * sms;  // as many CTAs as fit the SMs at a time
         const DevErr err = host_dev_err();
         if (e == cudaSuccess)
-            e = launch_pdl(rope_bulk_kernel, dim3((unsigned)(shares < most ? shares : most)), dim3(RP_THREADS), smem, st, 1, a,
-                           (int)shares, angles_max, err);
+            e = launch_pdl(rope_bulk_kernel, dim3((unsigned)(shares < most ? shares : most)), dim3(RP_THREADS), smem, st, 1,
+                           a, (int)shares, angles_max, err);
     } else {
         e = a.wide ? launch_pdl(rope_wide_kernel, dim3((unsigned)shares), dim3(RP_THREADS), 0, st, 1, a)
                    : launch_pdl(rope_single_kernel, dim3((unsigned)shares), dim3(RP_THREADS), 0, st, 1, a);
@@ -734,11 +731,11 @@ li_status launch_rope(RopeArgs a, cudaStream_t st) {
 }
 
 li_status launch_kv4_write(const Kv4Args& a, cudaStream_t st) {
-    const bool many = a.n >= K4_MANY;
-    const dim3 grid(ceil_div(a.n, K4_THREADS / 32 * (many ? 4 : 1))), block(K4_THREADS);
-    const cudaError_t e = !a.wide ? launch_pdl(kv4_write_kernel<false, 1>, dim3(ceil_div(a.n, K4_THREADS / 32)), block, 0, st, 1, a)
-                          : many  ? launch_pdl(kv4_write_kernel<true, 4>, grid, block, 0, st, 1, a)
-                                  : launch_pdl(kv4_write_kernel<true, 1>, grid, block, 0, st, 1, a);
+    const int rows = a.wide && a.n >= K4_MANY ? 2 : 1;
+    const dim3 grid(ceil_div(a.n, K4_THREADS / 32 * rows)), block(K4_THREADS);
+    const cudaError_t e = !a.wide     ? launch_pdl(kv4_write_kernel<false, 1>, grid, block, 0, st, 1, a)
+                          : rows == 1 ? launch_pdl(kv4_write_kernel<true, 1>, grid, block, 0, st, 1, a)
+                                      : launch_pdl(kv4_write_kernel<true, 2>, grid, block, 0, st, 1, a);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return LI_ERR_CUDA;
@@ -747,11 +744,7 @@ li_status launch_kv4_write(const Kv4Args& a, cudaStream_t st) {
 }
 
 li_status launch_kv4_read(const Kv4Args& a, cudaStream_t st) {
-    const bool many = a.n >= K4_MANY;
-    const dim3 grid(ceil_div(a.n, K4_THREADS / 32 * (many ? 4 : 1))), block(K4_THREADS);
-    const cudaError_t e = many ? launch_pdl(kv4_read_kernel<4>, grid, block, 0, st, 1, a)
-                               : launch_pdl(kv4_read_kernel<1>, grid, block, 0, st, 1, a);
-    if (e != cudaSuccess) {
+    if (launch_pdl(kv4_read_kernel, dim3(ceil_div(a.n, K4_THREADS / 32)), dim3(K4_THREADS), 0, st, 1, a) != cudaSuccess) {
         cudaGetLastError();
         return LI_ERR_CUDA;
     }
