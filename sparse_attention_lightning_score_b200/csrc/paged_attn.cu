@@ -39,8 +39,8 @@
 // TMEM has no room for their O), the weights between them about 1000, and the rows
 // of a pair (540 to 700 cycles to expand, about 1000 to gather) are hidden only
 // under the value products of the pairs behind it.  Measured: 3.06 us a tile of 64
-// heads in 4 bits (128 heads over a window of 131071: 69.5 us, 0.53 PFLOP/s), 2.83
-// in bf16 (1024 tokens x 128 heads, window 512: 292 us, 0.52 PFLOP/s).
+// heads in 4 bits (128 heads over a window of 131071: 67.3 us, 0.54 PFLOP/s), 2.83
+// in bf16 (1024 tokens x 128 heads, window 512: 281 us, 0.54 PFLOP/s).
 // With few units the visible tiles are split over several CTAs; a second kernel
 // merges the parts (see paged_attn_plan for the rule).
 #include <cuda_fp16.h>
@@ -233,10 +233,9 @@ __device__ __forceinline__ bool token_of(const PagedAttnArgs& a, int row, int* r
 
 __device__ __forceinline__ PaUnit unit_of(const PagedAttnArgs& a, int u, bool report) {
     PaUnit x;
-    x.hg = u % a.hgroups;
-    const int v = u / a.hgroups;
-    const int split = v % a.splits;
-    x.row = v / a.splits;
+    const unsigned v = (unsigned)u / (unsigned)a.hgroups, split = v % (unsigned)a.splits;
+    x.hg = (int)((unsigned)u - v * (unsigned)a.hgroups);
+    x.row = (int)(v / (unsigned)a.splits);
     int p;
     x.live = token_of(a, x.row, &x.req, &p, report);
     x.nsink = 0;
@@ -249,9 +248,11 @@ __device__ __forceinline__ PaUnit unit_of(const PagedAttnArgs& a, int u, bool re
         x.n = x.nsink + (p + 1 - w0);
     }
     if (!x.live) x.n = 0;
-    const int nt = (x.n + PA_M - 1) / PA_M;
-    x.t0 = (int)((long long)nt * split / a.splits);
-    x.t1 = (int)((long long)nt * (split + 1) / a.splits);
+    // (at most 2^21 tiles, and no more splits than units of four waves: 32 bits hold the product, and a 64-bit
+    // division would take longer than a load)
+    const unsigned nt = (unsigned)(x.n + PA_M - 1) / PA_M;
+    x.t0 = (int)(nt * split / (unsigned)a.splits);
+    x.t1 = (int)(nt * (split + 1) / (unsigned)a.splits);
     return x;
 }
 
@@ -503,6 +504,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // thread's part of tile np + 1 is read (4 bits), the page of np + 2 and the position of np + 3.
         PaWalk w;
         w.start(a);
+        // Tiles of a unit, < 0 for padding: looked up while the unit before still has its value product to wait for (at
+        // the head of each unit the loads and divisions took 1700 cycles: 292 -> 281 us for 1024 tokens x 128 heads).
+        const auto tiles_of = [&](int u) {
+            if (u >= a.units) return -1;
+            const PaUnit x = unit_of(a, u, threadIdx.x == 0);
+            return x.live ? x.t1 - x.t0 : -1;
+        };
+        int tiles = tiles_of(blockIdx.x);
         PaEntry e1{-1, -1, -1}, e2{-1, -1, -1};
         uint4 code[FP4 ? 4 : 1];
         uint2 sc = make_uint2(0, 0);                // 4 bits: pair 2 hi + half's eight scales
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             if constexpr (FP4) {
                 const uint8_t* from = here ? static_cast<const uint8_t*>(a.cache) + slot * LI_KV4_ROW_BYTES : nullptr;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) code[p] = early16(from ? from + p * 64 + hi * 32 + half * 16 : nullptr);
+                for (int p = 0; p < 3; ++p) code[p] = early16(from ? from + p * 64 + hi * 32 + half * 16 : nullptr);
                 sc = early8(from ? from + 256 + (2 * hi + half) * 8 : nullptr);
             }
             e1 = e2;
@@ -553,6 +562,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, src, 2 * (4 * group + i));
             if constexpr (FP4) {
+                // (the last pair's codes, a tile's time late: they are wanted last, and registers are short)
+                const uint8_t* from =
+                    here ? static_cast<const uint8_t*>(a.cache) + (long long)src * LI_KV4_ROW_BYTES : nullptr;
+                code[3] = early16(from ? from + 3 * 64 + hi * 32 + half * 16 : nullptr);
                 uint32_t sw[4];
 #pragma unroll
                 for (int p = 0; p < PA_PAIRS - 1; ++p) {
@@ -616,13 +629,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         }
 
         uint32_t n = 0, units = 0;
-        for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            int tiles;
-            {
-                const PaUnit x = unit_of(a, u, threadIdx.x == 0);
-                if (!x.live) continue;
-                tiles = x.t1 - x.t0;
-            }
+        for (int u = blockIdx.x, next; ok && u < a.units; u += gridDim.x, tiles = next) {
+            if (tiles <= 0) next = tiles_of(u + gridDim.x);
+            if (tiles < 0) continue;
             // where the unit's output goes (worked out again at its end: registers are short)
             const int h0 = (u % a.hgroups) * NH + g * GH;
             const int nh = min(GH, a.heads - h0);   // heads of this group that exist (may be <= 0)
@@ -744,6 +753,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 if (!ok) break;
             }
             if (!ok) break;
+            next = tiles_of(u + gridDim.x);
             if (!mbar_wait(odone, units & 1, a.err)) { ok = false; break; }
             tc_fence_after();
             ++units;
