@@ -230,10 +230,16 @@ class DecodeLayerStack:
     latent cache [B,L,576] (li_sparse_attention -> out [B,Ha,512] fp32); optionally a dense block
     standing in for the rest of the layer (x [B,dm] @ W [dm,dn], cuBLAS via torch).  Inputs are seeded
     and synthetic; caches are distinct per layer so that no layer reads another's from L2.
+
+    With `page_size` the latent cache is paged and held in 4 bits, and the step does what a server's step
+    does around it: the new token of each request (position L - 1) gets its slot once a step
+    (li_block_tables), and each layer rotates its queries and the token's row (li_rope), appends the row
+    (li_kv4_write) and attends (li_paged_sparse_attention -> out [B,Ha,512] bf16).  Pages lie in random
+    order; a repeated step finds the same free pages and gives the same result.
     """
 
     def __init__(self, n_layers: int, B: int, L: int, k: int = 2048, heads: int = 64, att_heads: int = 128,
-                 dense: Optional[tuple] = None, device="cuda", seed: int = 0):
+                 dense: Optional[tuple] = None, device="cuda", seed: int = 0, page_size: Optional[int] = None):
         import torch
         from . import api, synth
         self.api = api
@@ -246,8 +252,12 @@ class DecodeLayerStack:
         self.w = [torch.randn(B, heads, device=device, generator=g) * 0.1 for _ in range(n_layers)]
         self.qa = [torch.randn(B, att_heads, 576, device=device, generator=g).to(torch.bfloat16)
                    for _ in range(n_layers)]
-        self.kv = [torch.randn(B, L, 576, device=device, generator=g).to(torch.bfloat16) for _ in range(n_layers)]
-        self.out = torch.empty(n_layers, B, att_heads, 512, device=device)
+        self.page_size = page_size
+        if page_size is None:
+            self.kv = [torch.randn(B, L, 576, device=device, generator=g).to(torch.bfloat16) for _ in range(n_layers)]
+            self.out = torch.empty(n_layers, B, att_heads, 512, device=device)
+        else:
+            self._paged_cache(att_heads, device, g)
         self.scale = 1.0 / 192 ** 0.5
         self.dense = None
         if dense is not None:
@@ -260,6 +270,31 @@ class DecodeLayerStack:
         self.sel = None
         self._ws = {}
 
+    def _paged_cache(self, att_heads, device, g):
+        import torch
+        B, L, page = self.B, self.L, self.page_size
+        blocks, held = -(-L // page), -(-(L - 1) // page)
+        pages = torch.randperm(B * blocks, device=device, generator=g).to(torch.int32).view(B, blocks)
+        self.num_pages = B * blocks
+        self.free_pages = pages[:, held:].flatten().contiguous()   # what the new tokens' pages come from
+        slots = (pages.long().repeat_interleave(page, 1)[:, :L - 1] * page
+                 + torch.arange(L - 1, device=device) % page).flatten()
+        self.block_table = pages.clone()
+        self.block_table[:, held:] = -1
+        self.kv, self.row = [], []
+        for _ in range(self.n):
+            rows = torch.randn(B * (L - 1), 576, device=device, generator=g).to(torch.bfloat16)
+            self.kv.append(self.api.li_kv4_write(rows, slots, self.api.li_kv4_cache(self.num_pages, page, device)))
+            self.row.append(torch.randn(B, 576, device=device, generator=g).to(torch.bfloat16))
+        self.rope = self.api.li_rope_table(64, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.seq_lens, self.new_lens = torch.full((B,), L, **i32), torch.ones(B, **i32)
+        self.step_map = dict(slots=torch.empty(B, dtype=torch.int64, device=device), positions=torch.empty(B, **i32),
+                             requests=torch.empty(B, **i32), starts=torch.empty(B + 1, **i32),
+                             free_next=torch.empty(1, **i32))
+        self.rotated = [torch.empty_like(self.qa[0]), torch.empty_like(self.row[0])]
+        self.out = torch.empty(self.n, B, att_heads, 512, device=device, dtype=torch.bfloat16)
+
     def bind(self, plan: Sequence[LayerPlan], overlap: bool = True, with_rest: bool = True) -> TwoStreamStep:
         """A TwoStreamStep over this stack for `plan` (selection buffers sized for it); the dense block
         runs after each layer's attention when the stack has one and `with_rest` is set."""
@@ -270,7 +305,9 @@ class DecodeLayerStack:
         self.scores = torch.empty(step.n_slots, self.B, (self.L + 3) // 4 * 4, dtype=torch.float32,
                                   device=self.out.device)
         self.hist = [self.api.li_decode_select_workspace(self.B, self.out.device, self.L) for _ in range(step.n_slots)]
-        self.att_ws = self.api.li_sparse_attention_workspace(self.B, self.qa[0].shape[1], self.k, self.out.device)
+        size = self.api.li_sparse_attention_workspace if self.page_size is None else \
+            self.api.li_paged_attention_workspace
+        self.att_ws = size(self.B, self.qa[0].shape[1], self.k, self.out.device)
         return step
 
     def _indexer(self, layer, slot, stream):
@@ -279,8 +316,22 @@ class DecodeLayerStack:
                                   stream=stream)
 
     def _attention(self, layer, slot, stream):
+        if self.page_size is not None:
+            return self._paged_attention(layer, slot, stream)
         self.api.li_sparse_attention(self.qa[layer], self.kv[layer], self.sel[slot], self.scale,
                                      out=self.out[layer], workspace=self.att_ws, stream=stream)
+
+    def _paged_attention(self, layer, slot, stream):
+        api, at = self.api, self.step_map
+        if layer == 0:   # once a step: every layer's cache has the same pages
+            api.li_block_tables(self.seq_lens, self.new_lens, self.block_table, self.free_pages, self.page_size,
+                                self.num_pages, self.B, **at, stream=stream)
+        q, row = api.li_rope([self.qa[layer], self.row[layer]], at["positions"], self.rope, offset=512,
+                             out=self.rotated, stream=stream)
+        api.li_kv4_write(row, at["slots"], self.kv[layer], stream=stream)
+        api.li_paged_sparse_attention(q, self.kv[layer], self.sel[slot], self.scale, block_table=self.block_table,
+                                      requests=at["requests"], out=self.out[layer], workspace=self.att_ws,
+                                      stream=stream)
 
     def _rest(self, layer, stream):
         import torch

@@ -584,6 +584,75 @@ def test_attention_on_another_stream_and_in_a_graph():
     assert api.li_get_last_error() == LI_OK
 
 
+def test_attention_two_calls_at_once_with_workspaces_of_their_own():
+    """Split plans on two streams: each call's parts lie in its own workspace; and a workspace that is too small is
+    not used."""
+    c = Case(6, 1, 64, 3000, 64, "kv4", seed=14)
+    q, kw = [c.q.to(DEV), (-c.q).to(DEV)], c.kw()
+    sel = torch.from_numpy(c.select(2048)).to(DEV)
+    want = [api.li_paged_sparse_attention(x, c.cache, sel, c.scale, **kw) for x in q]
+    ws = [api.li_paged_attention_workspace(6, 64, 2048, DEV) for _ in range(2)]
+    assert ws[0].numel() > 6 * 64 * 512 * 4
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(want[0]) for _ in range(2)]
+    for _ in range(20):
+        for i in range(2):
+            api.li_paged_sparse_attention(q[i], c.cache, sel, c.scale, out=outs[i], workspace=ws[i], stream=streams[i], **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)
+    assert torch.equal(api.li_paged_sparse_attention(q[0], c.cache, sel, c.scale, workspace=small, **kw), want[0])
+    assert api.li_get_last_error() == LI_OK
+
+
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+def test_attention_gives_the_same_bits_again(kind):
+    """No sum depends on the order in which CTAs run."""
+    c = Case(9, 2, 40, 1500, 16, kind, seed=21)
+    q, kw, pos = c.q.to(DEV), c.kw(), _i32(c.pos)
+    outs = [api.li_window_attention(q, c.cache, pos, c.scale, 1100, sinks=9, **kw) for _ in range(4)]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_attention_without_pages_or_rows():
+    q = torch.randn(2, 16, 576, device=DEV).to(torch.bfloat16)
+    for cache in (api.li_kv4_cache(0, 16), torch.empty(0, 16, 576, dtype=torch.bfloat16, device=DEV)):
+        table = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+        sel = torch.full((2, 5), -1, dtype=torch.int32, device=DEV)
+        assert (api.li_paged_sparse_attention(q, cache, sel, 0.1, block_table=table) == 0).all()
+        assert api.li_get_last_error() == LI_OK
+        sel[1, 2] = 7                              # a position whose page (0) does not exist
+        assert (api.li_paged_sparse_attention(q, cache, sel, 0.1, block_table=table) == 0).all()
+        assert api.li_get_last_error() == LI_ERR_BOUNDS
+        assert api.li_paged_sparse_attention(q[:0], cache, sel[:0], 0.1, block_table=table[:0]).shape == (0, 16, 512)
+        none = torch.empty(0, dtype=torch.int32, device=DEV)
+        assert api.li_window_attention(q[:0], cache, none, 0.1, 4, block_table=table[:0]).shape == (0, 16, 512)
+    assert api.li_get_last_error() == LI_OK
+
+
+def test_attention_over_slots_beyond_four_gigabytes():
+    """A cache of 4.6 GB: the bytes of its last rows lie past 32 bits."""
+    page, pages = 64, 173000
+    cache = torch.empty(pages, page, 416, dtype=torch.uint8, device=DEV)
+    table = torch.tensor([[pages - 1, 0, pages - 3, pages - 2]], dtype=torch.int32)
+    n = 4 * page - 5
+    g = torch.Generator().manual_seed(5)
+    rows = torch.randn(n, 576, generator=g).to(torch.bfloat16)
+    s = np.arange(n)
+    slots = torch.from_numpy(table.numpy()[0, s // page].astype(np.int64) * page + s % page).to(DEV)
+    api.li_kv4_write(rows.to(DEV), slots, cache)
+    held = oracle.kv4_unpack(oracle.kv4_pack(rows))
+    assert np.array_equal(api.li_kv4_read(cache, slots).double().cpu().numpy(), held)
+    q = torch.randn(1, 64, 576, generator=g).to(torch.bfloat16)
+    out = api.li_window_attention(q.to(DEV), cache, _i32([n - 1]), 0.06, n, block_table=table.to(DEV))
+    ref, mag, top = oracle.attention(q[0].double().numpy(), held, 0.06)
+    d = 2.0 ** -23 * (600 * top + 64 + n / 16)
+    err = np.abs(out[0].double().cpu().numpy() - ref)
+    assert np.all(err <= U * mag + U * np.abs(ref) + 2 * d[:, None] * mag)
+    assert api.li_get_last_error() == LI_OK
+
+
 def test_attention_refusals():
     c = Case(2, 1, 64, 100, 16, "kv4", seed=1)
     q, sel, kw = c.q.to(DEV), torch.from_numpy(c.select(50)).to(DEV), c.kw()
@@ -650,4 +719,48 @@ def test_from_lengths_to_attention(layer):
             err = np.abs(out[t].cpu().double().numpy() - ref)
             assert np.all(err <= U * mag + U * np.abs(ref) + 2 * d[:, None] * mag), (new, t)
         assert (out[sum(new):] == 5).all()
+    assert api.li_get_last_error() == LI_OK
+
+
+@pytest.mark.parametrize("L", [900, 897])          # the new token inside a page, and first of a new one
+def test_decode_layers_over_a_paged_4bit_cache(L):
+    """The decode step over layers, two streams, captured and replayed: each layer's output against the definition
+    on the cache that the step left."""
+    from sparse_attention_lightning_score_b200.schedule import DecodeLayerStack, StepGraph, mli_plan, priority_streams
+    B, H, k, page = 3, 24, 256, 64
+    stack = DecodeLayerStack(n_layers=3, B=B, L=L, k=k, att_heads=H, device=DEV, seed=2, page_size=page)
+    step = stack.bind(mli_plan(3, lag=1))
+    main, side = priority_streams()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        step.run(main, side)
+    torch.cuda.synchronize()
+    first = stack.out.clone()
+    table = _np(stack.block_table)
+    assert (np.sort(table.reshape(-1)) == np.arange(table.size)).all()
+    pos, rope = _i32([L - 1] * B), api.li_rope_table(64)
+    slots = table[:, (L - 1) // page] * page + (L - 1) % page
+    assert np.array_equal(_np(stack.step_map["slots"]), slots)
+    for layer, p in enumerate(step.plan):
+        raw = _np(stack.kv[layer]).reshape(-1, 416)
+        # the rotated rows and queries as the device holds them (their rounding is checked by the rotation's own tests)
+        q, row = api.li_rope([stack.qa[layer], stack.row[layer]], pos, rope, offset=512)
+        assert np.array_equal(raw[slots], oracle.kv4_pack(row.cpu()))
+        slot = step.slots[p.attends]
+        assert max(i for i, w in enumerate(step.plan) if w.runs_indexer and step.slots[i] == slot) == p.attends
+        for b, s in enumerate(_lists(_np(stack.sel[slot]))):
+            s = s.astype(np.int64)
+            rows = oracle.kv4_unpack(raw[table[b, s // page].astype(np.int64) * page + s % page])
+            ref, mag, top = oracle.attention(q[b].cpu().double().numpy(), rows, stack.scale)
+            d = 2.0 ** -23 * (600 * top + 64 + len(s) / 16)
+            err = np.abs(first[layer, b].cpu().double().numpy() - ref)
+            assert len(s) == k and np.all(err <= U * mag + U * np.abs(ref) + 2 * d[:, None] * mag), (layer, b)
+    with torch.cuda.stream(main):
+        graph = StepGraph(step, main, side)
+        for _ in range(2):
+            stack.out.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(stack.out, first)
+    graph.close()
     assert api.li_get_last_error() == LI_OK
