@@ -257,9 +257,10 @@ __device__ __forceinline__ PaUnit unit_of(const PagedAttnArgs& a, int u, bool re
 }
 
 // A tile entry on its way to a row address, one dependent load a step.
+constexpr int PA_BEYOND = 0x7fffffff;  // (no request: those are below the number of requests)
 struct PaEntry {
     int s;              // position in the request, < 0: none
-    int req;
+    int req;            // PA_BEYOND: the list has ended before the warp's rows
     int page;           // of the cache, < 0: none
 };
 // Step 1: entry j of the unit's list.
@@ -271,7 +272,10 @@ __device__ __forceinline__ void entry_position(const PagedAttnArgs& a, const PaU
 // Step 2: its page.
 __device__ __forceinline__ void entry_page(const PagedAttnArgs& a, PaEntry& e) {
     e.page = -1;
-    if (e.s < 0) return;
+    if (e.s < 0) {
+        if (e.s < -1) record_error(a.err, ERRBIT_BOUNDS);
+        return;
+    }
     if ((long long)e.s >= (long long)a.max_blocks * a.page_size) {
         record_error(a.err, ERRBIT_BOUNDS);
         e.s = -1;
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             e.req = w.more ? 0 : -1;                // (-1: no such tile)
             if (w.more) {
                 entry_position(a, w.x, w.t * PA_M + r, e);
-                if (!FP4 && w.t * PA_M + (warp & ~1) * 8 >= w.x.n) e.s = -2;  // it ends before two warps' 16 rows
+                if (!FP4 && w.t * PA_M + (warp & ~1) * 8 >= w.x.n) e.req = PA_BEYOND;  // (16 rows of two warps)
                 w.next(a);
             }
         };
@@ -533,7 +537,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             more = e1.req >= 0;
             const long long slot = entry_slot(a, e1);
             here = slot >= 0;
-            src = here ? (int)slot : !FP4 && e1.s == -2 ? -1 : 0x7fffffff;  // (past every end: a gather fills in zeros)
+            // (no row: past every end, where a gather fills in zeros; -1: not even that)
+            src = here ? (int)slot : !FP4 && e1.req == PA_BEYOND ? -1 : 0x7fffffff;
             if constexpr (FP4) {
                 const uint8_t* from = here ? static_cast<const uint8_t*>(a.cache) + slot * LI_KV4_ROW_BYTES : nullptr;
 #pragma unroll

@@ -514,6 +514,23 @@ def test_attention_masks():
     assert api.li_get_last_error() == LI_OK
 
 
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+def test_attention_reports_negative_selections_other_than_none(kind):
+    """-2 and the lowest integer, alone among real positions and in place of whole runs, are skipped and reported."""
+    c = Case(3, 1, 64, 700, 16, kind, seed=31)
+    sel = c.select(400)
+    sel[0, ::3] = -2
+    sel[1, 64:200] = -2
+    sel[1, 300] = np.iinfo(np.int32).min
+    sel[2, 399] = -3
+    out = api.li_paged_sparse_attention(c.q.to(DEV), c.cache, torch.from_numpy(sel).to(DEV), c.scale, **c.kw())
+    assert api.li_get_last_error() == LI_ERR_BOUNDS
+    c.check(out, _lists(sel))
+    sel[sel < 0] = -1
+    again = api.li_paged_sparse_attention(c.q.to(DEV), c.cache, torch.from_numpy(sel).to(DEV), c.scale, **c.kw())
+    assert torch.equal(out, again) and api.li_get_last_error() == LI_OK
+
+
 def test_attention_dense_cache():
     """No block table: request r's positions are page r, as a dense [R, L] cache holds them."""
     c = Case(3, 1, 64, 500, 500, "bf16", seed=4)
