@@ -525,7 +525,7 @@ def li_block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     tokens of each request), block_table int32 [R, max_blocks] (extended in place), free_pages int32
     [n] (taken from entry free_start[0] on) -> (slots int64 [max_tokens], positions int32
     [max_tokens], requests int32 [max_tokens], starts int32 [R + 1], free_next int32 [1]); token entries
-    past the last new token are -1."""
+    past the last new token are -1.  (Outputs that the call makes share one allocation.)"""
     if stream is not None:
         with _under(stream, seq_lens):
             return _bind.block_tables(seq_lens, new_lens, block_table, free_pages, page_size, num_pages, max_tokens,

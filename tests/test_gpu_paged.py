@@ -623,6 +623,47 @@ def test_attention_two_calls_at_once_with_workspaces_of_their_own():
     assert api.li_get_last_error() == LI_OK
 
 
+def test_out_of_memory_is_torchs_own_error():
+    """A call whose output the allocator refuses raises what torch raises, and the next call works."""
+    cache = api.li_kv4_cache(4, 16)
+    slots = torch.zeros(1 << 21, dtype=torch.int64, device=DEV)        # (out: 2.4 GB)
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 29)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            api.li_kv4_read(cache, slots)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert (api.li_kv4_read(cache, slots[:7]) == 0).all() and api.li_get_last_error() == LI_OK
+
+
+def test_new_outputs_of_a_call_are_apart_and_outlive_each_other():
+    """Outputs that share an allocation: any of them can be written, kept or dropped without the others."""
+    g = torch.Generator().manual_seed(8)
+    xs = [torch.randn(s, generator=g).to(t).to(DEV) for s, t in
+          [((5, 3, 64), torch.bfloat16), ((5, 64), torch.float32), ((5, 7, 100), torch.bfloat16), ((5, 1, 66), torch.float32)]]
+    pos, table = _i32([0, 9, -1, 70000, 3]), api.li_rope_table(64)
+    live = [0, 1, 3, 4]
+    want = [torch.zeros_like(x) for x in xs]
+    api.li_rope(xs, pos, table, out=want)
+    outs = api.li_rope(xs, pos, table)
+    assert all(o.is_contiguous() and o.shape == x.shape and o.dtype == x.dtype for o, x in zip(outs, xs))
+    assert all(torch.equal(o[live], w[live]) for o, w in zip(outs, want))
+    outs[1].fill_(5)
+    assert all(torch.equal(outs[i][live], want[i][live]) for i in (0, 2, 3))
+    last = outs.pop()
+    del outs
+    torch.full((1 << 16,), 7.0, device=DEV)
+    assert torch.equal(last[live], want[3][live])
+    assert api.li_rope(xs[0][:0], pos[:0], table).shape == (0, 3, 64)
+    tables = api.li_block_tables(_i32([5, 2]), _i32([1, 2]), _i32([[3, -1], [-1, -1]]), _i32([6, 7]), 4, 8, 3)
+    got = [_np(x) for x in tables]
+    tables[0].fill_(-9)
+    assert all(np.array_equal(_np(x), w) for x, w in zip(tables[1:], got[1:])) and got[3].tolist() == [0, 1, 3]
+    assert api.li_get_last_error() == LI_OK
+
+
 @pytest.mark.parametrize("kind", ["kv4", "bf16"])
 def test_attention_gives_the_same_bits_again(kind):
     """No sum depends on the order in which CTAs run."""
