@@ -653,6 +653,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 }
                 continue;
             }
+            const bool whole = a.splits == 1;
+            const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;  // [row][split][head]
             float m_run[PASSES];      // of head h0 + HB pass + lane % HB, the same in the group's four warps
             float l[GH];              // sums over this thread's positions, per head
 #pragma unroll
@@ -754,6 +756,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pready);
+                if (t == tiles - 1) {  // the sums, while the value product runs
+                    warp_reduce_scatter<false>(l, lane);
+                    if (lane < GH) wm[lane] = l[0];  // (another warp may still read the maxima in red)
+                    group_sync(bar);
+                    const float* parts = msm + g * 4 * GH + lane % GH;
+                    const float sum = (parts[0] + parts[GH]) + (parts[2 * GH] + parts[3 * GH]);
+                    group_sync(bar);
+                    if (!whole && q4 == 0 && lane < nh) {
+                        // (m_run is of head lane % HB)
+                        const float m = PASSES == 1 || lane < HB ? m_run[0] : m_run[PASSES - 1];
+                        // without a maximum the sum is 0 (nothing visible) or NaN, which the merge must not drop
+                        a.mpart[part + lane] = m == -INFINITY && sum != 0.f ? 0.f : m;
+                        a.lpart[part + lane] = sum;
+                    }
+                    if (lane < GH) wm[lane] = sum == 0.f ? 0.f : 1.f / sum;
+                    __syncwarp();
+                }
                 if (more) bring();
                 if (!ok) break;
             }
@@ -762,22 +781,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             if (!mbar_wait(odone, units & 1, a.err)) { ok = false; break; }
             tc_fence_after();
             ++units;
-            warp_reduce_scatter<false>(l, lane);
-            if (lane < GH) gred[q4 * GH + lane] = l[0];
-            group_sync(bar);
-            const int k16 = lane % GH;
-            const float sum = (gred[k16] + gred[GH + k16]) + (gred[2 * GH + k16] + gred[3 * GH + k16]);
-            group_sync(bar);  // red is written again by the next unit
-            const bool whole = a.splits == 1;
-            const size_t part = (size_t)(u / a.hgroups) * a.heads + h0;  // [row][split][head]
-            if (!whole && q4 == 0 && lane < nh) {
-                const float m = PASSES == 1 || lane < HB ? m_run[0] : m_run[PASSES - 1];  // (lane % HB is lane's)
-                // without a maximum the sum is 0 (nothing visible) or NaN, which the merge must not drop
-                a.mpart[part + lane] = m == -INFINITY && sum != 0.f ? 0.f : m;
-                a.lpart[part + lane] = sum;
-            }
-            if (lane < GH) wm[lane] = sum == 0.f ? 0.f : 1.f / sum;
-            __syncwarp();
             float fac[GH];
             read_factors(wm, fac);
 #pragma unroll 1
