@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         tmem_alloc(tmem_slot, L::TMEM_COLS);
         tmem_relinquish();
     }
-    if (a.splits > 1) pdl_trigger();  // the merge may be placed (it waits for this kernel's end)
+    pdl_trigger();  // the merge, or the stream's next kernel, may be placed (it waits for this kernel's end)
     pdl_wait();  // the query, the selection and the cache may come from the previous kernel of the stream
     tc_fence_before();
     __syncthreads();
@@ -841,6 +841,7 @@ __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedA
     const int h = blockIdx.x, row = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int stripe = tid / LANES, d = blockIdx.y * (PA_DV / ST) + tid % LANES * 4;
     pdl_wait();
+    pdl_trigger();
     int r, p;
     if (!token_of(a, row, &r, &p, false)) return;
     const size_t at = (size_t)row * a.splits * a.heads + h;
