@@ -7,7 +7,7 @@
 // shared by every head).  A row is held in 4 bits (LI_KV4_ROW_BYTES: 512 e2m1
 // codes, one e4m3 scale per 16 of them, 64 bf16) or as 576 bf16.  e2m1 x e4m3
 // has 6 significant bits, so a 4-bit row is expanded to bf16 exactly and the
-// two formats share everything behind the producer warps.
+// two formats share everything behind the rows' expansion.
 //
 // One CTA (one per SM, persistent) takes units of one token, 64, 32 or 16 heads and
 // a share of the token's visible positions, 128 positions (a tile) at a time.
@@ -38,9 +38,10 @@
 // 68 products take 48 cycles each at 64 heads (40 at 32 or 16; at 128 heads 64, but
 // TMEM has no room for their O), the weights between them about 1000, and the rows
 // of a pair (540 to 700 cycles to expand, about 1000 to gather) are hidden only
-// under the value products of the pairs behind it.  Measured: 3.06 us a tile of 64
-// heads in 4 bits (128 heads over a window of 131071: 67.3 us, 0.54 PFLOP/s), 2.83
-// in bf16 (1024 tokens x 128 heads, window 512: 281 us, 0.54 PFLOP/s).
+// under the value products of the pairs behind it.  Measured: 2.8 us a tile of 64
+// heads in 4 bits with few CTAs, 3.5 with all SMs busy (128 heads over a window of
+// 131071: 68 us, 0.54 PFLOP/s); bf16 2.7 and 3.4 (1024 tokens x 128 heads, window
+// 512: 280 us, 0.54 PFLOP/s).
 // With few units the visible tiles are split over several CTAs; a second kernel
 // merges the parts (see paged_attn_plan for the rule).
 #include <cuda_fp16.h>
@@ -930,11 +931,11 @@ li_status launch_units(const CUtensorMap& qmap, const CUtensorMap& kmap, const P
 // in microseconds.  Units run in waves of one per SM; a unit costs its tiles and a start and end that grow with
 // its heads (the end writes them); parts cost a merge, and their fp32 sums are written and read once more.  For
 // each number of waves the largest count of splits that fits is tried, lowered as far as the longest share stays
-// the same.  Measured, 4-bit rows, 64 / 32 / 16 heads a unit: a tile 3.06 / 2.42 / 2.37 (bf16 rows 2.83 / 2.33 /
-// 2.15).  What the rule decides between, as measured: 1 token x 64 heads, 2048 rows: 16 heads in 16 splits 12.4, 64
-// heads in 16 splits 15.8; 8 x 128, 2048 rows: 64 in 8 23.0, 32 in 4 24.2, 16 in 2 32.6; 32 x 128, 516 rows: 32 unsplit
-// 22.1, 64 in 2 26.1, 64 unsplit 26.7; 74 x 16, 1000 rows: 16 in 2 21.7, unsplit 28.4; 1 x 128, 131071 rows: 64 in 74
-// 70, 32 in 74 101.
+// the same.  The constants are fitted to whole calls; a further tile alone takes 2.8 / 2.2 / 2.0 us at 64 / 32 / 16
+// heads a unit with 4-bit rows (bf16: 2.7 / 2.2 / 2.1).  What the rule decides between, as measured: 1 token x 64 heads,
+// 2048 rows: 16 heads in 16 splits 11.5, 64 heads in 16 splits 14.5; 8 x 128, 2048 rows: 64 in 8 22.3, 32 in 4 23.3, 16
+// in 2 31.9; 32 x 128, 516 rows: 32 unsplit 20.4, 64 in 2 24.8, 64 unsplit 24.9; 74 x 16, 1000 rows: 16 in 2 20.9,
+// unsplit 27.0; 1 x 128, 131071 rows: 64 in 74 68, 32 in 74 98, 64 in 148 84.
 PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms) {
     const int tiles = (positions + PA_M - 1) / PA_M;
     static const struct {
