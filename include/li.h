@@ -596,7 +596,9 @@ typedef struct {
  * A token with no valid selection gets 0.  Selections outside [0, max_blocks *
  * page_size) or in a page outside the cache are skipped and reported as
  * LI_ERR_BOUNDS by li_get_last_error; a request outside [0, requests) is reported and
- * its token treated as padding.  Positions nothing selects are never read. */
+ * its token treated as padding.  Positions nothing selects are never read.
+ * LI_ERR_UNSUPPORTED: more than 4096 heads, more than 2^28 selections or visible positions,
+ * or a cache of 2^31 - 1 rows or more. */
 li_status li_paged_sparse_attention(const void* q_bf16, const void* cache, const int32_t* block_table,
                                     const int32_t* requests_of, const int32_t* sel, int k, const li_attn_desc* desc,
                                     void* out_bf16, void* workspace, size_t workspace_bytes, li_stream_t stream);

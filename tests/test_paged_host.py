@@ -143,6 +143,12 @@ def test_paged_attention_rejects_bad_arguments():
     assert _window(d, max_len=65) == BAD and _window(d, pos=None) == BAD   # longer than the block table
 
 
+def test_paged_attention_limits():
+    assert _sparse(_desc(), k=(1 << 28) + 1) == NO
+    assert _sparse(_desc(num_pages=1 << 25, page_size=64)) == NO      # 2^31 rows
+    assert _window(_desc(max_blocks=1 << 26), window=1 << 29, max_len=1 << 29) == NO
+
+
 def test_paged_attention_workspace_size():
     f = _lib.load().li_paged_attention_workspace
     assert f(0, 64, 10) == 0 and f(2, 0, 10) == 0 and f(2, 64, 0) == 0
