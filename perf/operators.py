@@ -329,7 +329,7 @@ def _plain_kv4(s):
 def _attend(s, at, valid):
     """Attention of each token over positions `at` [n, m] of its request where `valid`."""
     p = s["case"]["page"]
-    at = at.clamp(0, s["table"].shape[1] * p - 1).long()   # (masked entries may lie outside the request)
+    at = at.clamp(min=0).long()
     slot = s["table"][s["requests"].long()[:, None], at // p].long() * p + at % p
     raw = s["cache"].flatten(0, 1)[slot]
     kv = (_unpack4(raw) if s["case"]["cache"] == "kv4" else raw.float()).masked_fill(~valid[:, :, None], 0.0)
