@@ -128,6 +128,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
 // stream is still running; pdl_wait() blocks the calling thread until that
 // kernel has completed and its memory is visible (a no-op without the
 // attribute).  pdl_trigger() lets the next kernel of the stream be scheduled.
+// Tensor memory is allocated behind pdl_wait(): a kernel that holds some while it
+// waits could hold what an earlier one on the SM still needs, and each would wait for
+// the other.  The two streaming scorers do allocate before they wait (schedules with
+// two scorers in flight lose 3 to 9 % otherwise); a third scorer, or an attention
+// CTA beside one, does not fit an SM's shared memory, and two of them need no more
+// than all of its tensor memory, so no scorer ever lacks it (asserted where they are).
+constexpr int kSmemPerSm = 228 * 1024;
+constexpr int kScorerSmem = kSmemPerSm / 3 + 1;  // least shared memory of a scorer's CTA
+constexpr int kScorerTmem = 256;                 // its most tensor memory, in columns
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -45,6 +45,8 @@ constexpr int L8_PRO_WARPS = 8;
 constexpr int L8_THREADS = 64 + 32 * L8_PRO_WARPS;
 
 __host__ __device__ constexpr int l8_smem(bool hist) { return L8_OFF_HIST + (hist ? LI_HIST_BINS * 4 : 0) + 1024; }
+static_assert(l8_smem(false) >= kScorerSmem && L8_NACC * L8_H <= kScorerTmem,
+              "tensor memory held while waiting (see pdl_wait)");
 
 __device__ __forceinline__ uint8_t* l8_align1024(uint8_t* p) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));

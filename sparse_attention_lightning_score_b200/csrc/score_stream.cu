@@ -58,7 +58,8 @@ struct StreamCfg {
     static constexpr int PRO_WARPS = FP8 ? 8 : 4;
     static constexpr int THREADS = 64 + 32 * PRO_WARPS;
     static constexpr int ELEMS_PER_KBLOCK = FP8 ? 128 : 64;
-    static_assert(TMEM_COLS == 128 || TMEM_COLS == 256 || TMEM_COLS == 512, "TMEM columns");
+    static_assert(TMEM_COLS == 128 || TMEM_COLS == 256, "TMEM columns");
+    static_assert(SMEM >= kScorerSmem && TMEM_COLS <= kScorerTmem, "tensor memory held while waiting (see pdl_wait)");
 };
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {

@@ -68,6 +68,7 @@ constexpr int NBAR = 2 * SA_RS + 3 + SA_NT;
 constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr int SA_SMEM = OFF_TMEM + 16 + 1024;           // + slack to align the base to 1024
 static_assert(SA_SMEM <= 232448, "shared memory per CTA");
+static_assert(SA_SMEM + kScorerSmem > kSmemPerSm, "no scorer beside it (see pdl_wait)");
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -154,11 +155,11 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         mbar_init(odone, 1);
         fence_mbar_init();
     }
-    if (warp == 4) {
+    pdl_wait();  // the selections may come from the previous kernel of the stream
+    if (warp == 4) {  // (behind the wait: see pdl_wait)
         tmem_alloc(tmem_slot, SA_TMEM_COLS);
         tmem_relinquish();
     }
-    pdl_wait();  // the selections may come from the previous kernel of the stream
     if (threadIdx.x == 0) {
         // the 64 query rows of the CTA's heads, first of all (nothing can be consumed before them)
         mbar_arrive_expect_tx(qfull, SA_CH * SA_QCHUNK);
