@@ -590,7 +590,8 @@ typedef struct {
  *   sel          [rows, k] int32 positions in the token's request (li_topk's output, any
  *                order; -1 = none; one listed twice counts twice)
  *   out_bf16     [rows, heads, 512] bf16, 16-byte aligned.  The softmax weights are
- *                rounded to bf16 for the value product, sums and statistics are fp32.
+ *                rounded to bf16 for the value product and divided by the fp32 sum of the
+ *                rounded ones; the other statistics are fp32.
  *   workspace    li_paged_attention_workspace(rows, heads, k) bytes, 256-byte aligned
  *                (may be 0: then NULL).  Calls that overlap in time must not share one.
  * A token with no valid selection gets 0.  Selections outside [0, max_blocks *

@@ -25,8 +25,10 @@
 //     warps.  The running maximum of a head is raised only when a tile exceeds it by
 //     more than 2^8 (p stays below 2^8, which bf16 and the fp32 sums hold as exactly
 //     as p <= 1), so after a unit's first tile no maximum is exchanged and O is
-//     rescaled in TMEM almost never.  Sums are fp32; p is rounded to bf16 for the
-//     product (2^-9 to 2^-8 of it, the same step as the bf16 output's).
+//     rescaled in TMEM almost never.  p is rounded to bf16 for the product (at most 2^-8
+//     of it, the same step as the bf16 output's); the fp32 sums are of the rounded p, so
+//     the weights that the rows get sum to one, and what the rows have in common comes
+//     through unchanged.
 //   - Warp 16 issues S^T = K Q^T (M = 128 positions, N = the unit's heads, K = 576) and
 //     O^T += V^T P^T (M = 128 latent elements, four blocks, K = 128), both
 //     from the same chunks: K is read K-major, V^T MN-major, so nothing is loaded
@@ -754,7 +756,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                         *reinterpret_cast<uint2*>(ps + sw128_offset(row, g >> 1) + 8 * (g & 1)) =
                             make_uint2(pk[0], pk[1]);
 #pragma unroll
-                    for (int i = 0; i < HB; ++i) l[pass * HB + i] += __uint_as_float(s[i]);
+                    for (int j = 0; j < HB / 2; ++j) {  // (what the product takes, not what was rounded to it)
+                        l[pass * HB + 2 * j] += __uint_as_float(pk[j] << 16);
+                        l[pass * HB + 2 * j + 1] += __uint_as_float(pk[j] & 0xffff0000u);
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();

@@ -1,10 +1,12 @@
-"""Paged-cache operators at edges: tensors that share a buffer.  Definitions: oracle.paged."""
+"""Paged-cache operators at edges: tensors that share a buffer, values that all rows have in common.  Definitions:
+oracle.paged."""
+import numpy as np
 import pytest
 import torch
 
 from sparse_attention_lightning_score_b200 import api
 from sparse_attention_lightning_score_b200._lib import LI_OK
-from tests.test_gpu_paged import DEV, _i32
+from tests.test_gpu_paged import DEV, Case, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +31,22 @@ def test_rope_tensors_of_a_call_that_share_a_buffer():
         api.li_rope([heads[:, 2:], heads[:, :3]], pos, table, out=[heads[:, 2:], torch.empty(3, 3, 128, device=DEV,
                                                                                              dtype=torch.bfloat16)])
     assert torch.equal(fused, old)
+
+
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+@pytest.mark.parametrize("R,H,L,k", [(1, 64, 300, 300), (2, 128, 3000, 2048), (40, 256, 600, 512), (80, 16, 1100, 1000),
+                                     (150, 8, 500, 400), (3, 100, 900, 900)])
+def test_attention_gives_back_what_all_rows_have_in_common(kind, R, H, L, k):
+    """Every row has the same latent elements and only the rotary ones differ: whatever the weights, the output is
+    those elements.  They are bf16, and fp32 sums of at most 2048 terms are off by less than 2^-12 of the value, below
+    the half step of 2^-9 and more at which the output's rounding would leave it."""
+    c = Case(R, 1, H, L, 64, kind, seed=R + k, scale=0.3,
+             shape=lambda x: torch.cat([x[:1, :512].expand(x.shape[0], -1), x[:, 512:] * 3], 1))
+    sel = c.select(k)
+    q = c.q.to(DEV)
+    want = torch.from_numpy(c.rows[0, :512]).to(torch.bfloat16).to(DEV)
+    assert np.array_equal(want.double().cpu().numpy(), c.rows[0, :512])
+    out = api.li_paged_sparse_attention(q, c.cache, torch.from_numpy(sel).to(DEV), c.scale, **c.kw())
+    assert (out == want).all()
+    out = api.li_window_attention(q, c.cache, _i32(c.pos), c.scale, k, sinks=3, **c.kw())
+    assert (out == want).all() and api.li_get_last_error() == LI_OK
