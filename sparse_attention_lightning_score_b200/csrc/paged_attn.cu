@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     if (!whole && q4 == 0 && lane < nh) {
                         // (m_run is of head lane % HB)
                         const float m = PASSES == 1 || lane < HB ? m_run[0] : m_run[PASSES - 1];
-                        // without a maximum the sum is 0 (nothing visible) or NaN, which the merge must not drop
+                        // without a maximum the sum is 0 (nothing visible) or NaN, which the merge does not drop
                         a.mpart[part + lane] = m == -INFINITY && sum != 0.f ? 0.f : m;
                         a.lpart[part + lane] = sum;
                     }
@@ -841,6 +841,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 // of 24 tokens x 128 heads in 3 parts: 25.4 us, 32.1 with ST = 4; 8 x 128 in 8: 21.8 and 22.6), ST = 4 shortens the walk
 // over more than eight parts (1 x 64 in 16 parts: 12.2 us, 13.2 with ST = 1; 1 x 128 in 74: 66.7 and 82.2).
 constexpr int PA_MERGE = 128;
+constexpr float PA_UNWRITTEN = -1.f;  // weight of a part without a visible position: it has not been written
 template <int ST>
 __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedAttnArgs a) {
     constexpr int LANES = PA_MERGE / ST;
@@ -866,9 +867,10 @@ __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedA
     top = fmaxf(fmaxf(wred[0][0], wred[0][1]), fmaxf(wred[0][2], wred[0][3]));
     float sum = 0.f;
     for (int s = tid; s < a.splits; s += PA_MERGE) {
-        const float f = top == -INFINITY || weight[s] == -INFINITY ? 0.f : pa_ex2(weight[s] - top);
+        // (a weight that underflows still counts: a NaN in its sum or values comes through, as it does without parts)
+        const float f = weight[s] == -INFINITY ? PA_UNWRITTEN : pa_ex2(weight[s] - top);
         weight[s] = f;
-        if (f != 0.f) sum += f * a.lpart[at + (size_t)s * a.heads];
+        if (f != PA_UNWRITTEN) sum += f * a.lpart[at + (size_t)s * a.heads];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -880,9 +882,8 @@ __global__ void __launch_bounds__(PA_MERGE) paged_attn_merge_kernel(const PagedA
 #pragma unroll 8
     for (int s = stripe; s < a.splits; s += ST) {
         const float f = weight[s];
-        // (a part without a visible position has not been written)
-        const float4 o = f != 0.f ? *reinterpret_cast<const float4*>(src + (size_t)s * a.heads * PA_DV)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (f == PA_UNWRITTEN) continue;
+        const float4 o = *reinterpret_cast<const float4*>(src + (size_t)s * a.heads * PA_DV);
         acc.x += f * o.x;
         acc.y += f * o.y;
         acc.z += f * o.z;

@@ -1,5 +1,5 @@
-"""Paged-cache operators at edges: tensors that share a buffer, values that all rows have in common.  Definitions:
-oracle.paged."""
+"""Paged-cache operators at edges: tensors that share a buffer, values that all rows have in common, NaN far
+below the maximum.  Definitions: oracle.paged."""
 import numpy as np
 import pytest
 import torch
@@ -50,3 +50,30 @@ def test_attention_gives_back_what_all_rows_have_in_common(kind, R, H, L, k):
     assert (out == want).all()
     out = api.li_window_attention(q, c.cache, _i32(c.pos), c.scale, k, sinks=3, **c.kw())
     assert (out == want).all() and api.li_get_last_error() == LI_OK
+
+
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+@pytest.mark.parametrize("where", [(5,), tuple(range(128)), (2047,)])
+@pytest.mark.parametrize("R,H", [(1, 64), (8, 128), (40, 256)])
+def test_attention_nan_far_below_the_maximum_is_passed_on(kind, where, R, H):
+    """A visible NaN row, or a tile of nothing else, among logits so far below the maximum that their weights
+    underflow: every head is NaN, in parts (the first two) or in one piece (the last)."""
+    L = 2048
+    level = torch.full((L, 1), 40.0)
+    level[:128], level[1900:] = -40.0, -40.0
+    c = Case(R, 1, H, L, L, kind, seed=3, scale=0.3,
+             shape=lambda x: torch.cat([x[:, :512], level.repeat(x.shape[0] // L, 1).expand(-1, 64)], 1))
+    c.lens, c.pos = [L] * R, [L - 1] * R
+    q = torch.cat([c.q[:, :, :512] * 0.05, c.q[:, :, 512:].abs() + 0.1], 2).to(torch.bfloat16).to(DEV)
+    sel = torch.arange(L, dtype=torch.int32, device=DEV).expand(R, L).contiguous()
+    clean = api.li_paged_sparse_attention(q, c.cache, sel, c.scale, **c.kw())
+    assert not clean.isnan().any()
+    rows = c.cache[int(c.table[0, 0])]
+    if kind == "bf16":
+        rows[list(where)] = float("nan")
+    else:
+        rows[list(where), 256:288] = 127           # every scale NaN
+    out = api.li_paged_sparse_attention(q, c.cache, sel, c.scale, **c.kw())
+    assert out[0].isnan().all() and torch.equal(out[1:], clean[1:])
+    out = api.li_window_attention(q, c.cache, _i32(c.pos), c.scale, L, **c.kw())
+    assert out[0].isnan().all() and torch.equal(out[1:], clean[1:])
