@@ -505,7 +505,8 @@ li_status li_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int 
  *                   beta_fast, a linear ramp over the pairs in between (its ends
  *                   rounded outward to whole pairs, as YaRN defines them)
  * turns (HOST memory, [rot_dim / 2]): f_i / (2 pi) turns, modulo 1, as 64-bit
- * fixed-point fractions.  The caller uploads them once.  rot_dim even, 2..1024;
+ * fixed-point fractions, each within 2^-63 turns of the formula's value.  The caller
+ * uploads them once.  rot_dim even, 2..1024;
  * base > 1; factor >= 1; original_len >= 1 and beta_fast > beta_slow > 0 (YaRN). */
 typedef enum { LI_ROPE_PLAIN = 0, LI_ROPE_LINEAR = 1, LI_ROPE_YARN = 2 } li_rope_scaling;
 li_status li_rope_table(int rot_dim, double base, int scaling, double factor, int original_len, double beta_fast,
@@ -532,8 +533,9 @@ typedef struct {
 /* Rotates up to four tensors of the same tokens (queries and keys, of the indexer
  * and of the attention) in one launch:
  *     (a, b) -> mscale * (a cos - b sin, a sin + b cos),  angle = position * f_i.
- * The rest of a head is copied, or left alone when out is x.  The angle is reduced
- * exactly; the rotation is computed in fp32 and rounded once.  A token whose position
+ * The rest of a head is copied, or left alone when out is x.  The angle is within
+ * position * 2^-63 + 2^-25 turns of the formula's; the rotation is computed in fp32 and
+ * rounded once.  A token whose position
  * is negative is padding: its row of out is left as it was.
  *   positions [tokens] int32      turns [rot_dim / 2] uint64 (device; li_rope_table)
  * Any strides and alignment (16-byte items where every one allows it); x and out are

@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <limits>
 
 #include "li_common.cuh"
 #include "li_kernels.cuh"
@@ -723,22 +724,25 @@ li_status li_rope_table(int rot_dim, double base, int scaling, double factor, in
     if (scaling == LI_ROPE_YARN &&
         (original_len < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !(beta_fast < 1e30)))
         return LI_ERR_INVALID_ARG;
-    const double two_pi = 6.283185307179586476925286766559;
+    // 64 significant bits at every step: a position times an error of 2^-53 of the frequency would show in fp32
+    static_assert(std::numeric_limits<long double>::digits >= 64, "the table's precision");
+    const long double two_pi = 6.283185307179586476925286766559005768L;
     double lo = 0.0, hi = 0.0;
     if (scaling == LI_ROPE_YARN) {
         // the (fractional) pair that makes beta turns over original_len positions
         auto pair_of = [&](double beta) {
-            return rot_dim * std::log(original_len / (beta * two_pi)) / (2.0 * std::log(base));
+            return rot_dim * std::log(original_len / (beta * (double)two_pi)) / (2.0 * std::log(base));
         };
         lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
         hi = std::fmin(std::ceil(pair_of(beta_slow)), rot_dim - 1.0);
     }
     for (int i = 0; i < rot_dim / 2; ++i) {
-        double f = std::pow(base, -2.0 * i / rot_dim);
+        long double f = std::pow((long double)base, -2.0L * i / rot_dim);
         if (scaling == LI_ROPE_LINEAR) f /= factor;
         if (scaling == LI_ROPE_YARN) {
-            const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
-            f = f / factor * ramp + f * (1.0 - ramp);
+            const long double span = std::fmax(hi - lo, 0.001);
+            const long double ramp = std::fmin(std::fmax((i - (long double)lo) / span, 0.0L), 1.0L);
+            f = f / factor * ramp + f * (1.0L - ramp);
         }
         turns[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 64));  // f <= 1: below 2^62
     }

@@ -162,9 +162,10 @@ __global__ void __launch_bounds__(BT_THREADS) block_table_kernel(const BlockTabl
 // ---------------------------------------------------------------------------
 // (a, b) -> m (a cos - b sin, a sin + b cos) with the angle pos * f_i.  A far position
 // times a frequency loses its fraction in fp32, so the frequency comes in turns as a
-// 64-bit fixed-point fraction: the product wraps modulo one turn by itself, exactly up
-// to pos * 2^-65 turns, and the top 32 bits are a signed fraction for sincospi (fp32
-// rounding of an angle within half a turn: 2^-25 turns).
+// 64-bit fixed-point fraction: the product wraps modulo one turn by itself.  The table
+// is within 2^-63 turns of the frequency, so the angle is within pos * 2^-63 turns, and
+// the top 32 bits are a signed fraction for sincospi (2^-33 turns, and the fp32 rounding
+// of an angle within half a turn: 2^-26 turns).
 // Two forms.  Few tokens, rows rotated in place, or heads spread out: a CTA takes one tensor's
 // run of heads of one token (or a few tokens with few heads); a thread keeps one place of a
 // head (an item: a 16-byte vector, or with the half layout two) and walks the rows (token,
