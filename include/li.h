@@ -507,7 +507,8 @@ li_status li_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int 
  * turns (HOST memory, [rot_dim / 2]): f_i / (2 pi) turns, modulo 1, as 64-bit
  * fixed-point fractions, each within 2^-63 turns of the formula's value.  The caller
  * uploads them once.  rot_dim even, 2..1024;
- * base > 1; factor >= 1; original_len >= 1 and beta_fast > beta_slow > 0 (YaRN). */
+ * base > 1; factor >= 1; beta_fast > beta_slow > 0 and original_len >= 2 pi beta_slow
+ * (YaRN: pair 0 makes beta_slow turns over original_len). */
 typedef enum { LI_ROPE_PLAIN = 0, LI_ROPE_LINEAR = 1, LI_ROPE_YARN = 2 } li_rope_scaling;
 li_status li_rope_table(int rot_dim, double base, int scaling, double factor, int original_len, double beta_fast,
                         double beta_slow, uint64_t* turns);

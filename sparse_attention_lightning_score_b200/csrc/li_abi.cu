@@ -729,6 +729,8 @@ li_status li_rope_table(int rot_dim, double base, int scaling, double factor, in
     const long double two_pi = 6.283185307179586476925286766559005768L;
     double lo = 0.0, hi = 0.0;
     if (scaling == LI_ROPE_YARN) {
+        // (where not even pair 0 makes beta_slow turns the ramp would end before it, and pair 0 keep its frequency)
+        if (original_len < beta_slow * (double)two_pi) return LI_ERR_INVALID_ARG;
         // the (fractional) pair that makes beta turns over original_len positions
         auto pair_of = [&](double beta) {
             return rot_dim * std::log(original_len / (beta * (double)two_pi)) / (2.0 * std::log(base));

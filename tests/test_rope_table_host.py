@@ -39,3 +39,15 @@ def test_table_is_within_two_units_of_the_fixed_point(rot, kw):
     got = api.li_rope_table(rot, device="cpu", **kw).tolist()
     for g, w in zip(got, _turns(rot, **kw)):
         assert abs(Decimal(g % 2 ** 64) - w) <= 2
+
+
+def test_yarn_needs_a_pair_that_makes_beta_slow_turns():
+    """Over fewer than 2 pi beta_slow positions every pair makes fewer than beta_slow turns and would be divided by the
+    factor, but the ramp, which starts at pair 0, would leave that one as it is: refused."""
+    kw = dict(scaling="yarn", factor=40.0, device="cpu")
+    for short, enough, slow in [(1, 7, 1.0), (6, 7, 1.0), (12, 13, 2.0), (3, 4, 0.5)]:
+        with pytest.raises(api.LiError):
+            api.li_rope_table(64, original_len=short, beta_slow=slow, **kw)
+        got = api.li_rope_table(64, original_len=enough, beta_slow=slow, **kw).tolist()
+        plain = api.li_rope_table(64, device="cpu").tolist()
+        assert got[0] == plain[0] and abs(got[31] - plain[31] / 40) <= 1 + plain[31] * 2.0 ** -52
