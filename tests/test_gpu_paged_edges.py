@@ -1,12 +1,13 @@
-"""Paged-cache operators at edges: tensors that share a buffer, values that all rows have in common, NaN far
-below the maximum.  Definitions: oracle.paged."""
+"""Paged-cache operators at edges: tensors that share a buffer, heads over several stages of a bulk copy,
+values that all rows have in common, NaN far below the maximum.  Definitions: oracle.paged."""
 import numpy as np
 import pytest
 import torch
 
+from oracle import paged as oracle
 from sparse_attention_lightning_score_b200 import api
 from sparse_attention_lightning_score_b200._lib import LI_OK
-from tests.test_gpu_paged import DEV, Case, _i32
+from tests.test_gpu_paged import DEV, Case, _check_rope, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -31,6 +32,32 @@ def test_rope_tensors_of_a_call_that_share_a_buffer():
         api.li_rope([heads[:, 2:], heads[:, :3]], pos, table, out=[heads[:, 2:], torch.empty(3, 3, 128, device=DEV,
                                                                                              dtype=torch.bfloat16)])
     assert torch.equal(fused, old)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("n,heads,dim,offset", [(301, 43, 192, 128), (301, 127, 192, 64), (67, 128, 576, 512)])
+def test_rope_heads_over_several_stages(dtype, layout, n, heads, dim, offset):
+    """Sizes that go by bulk copies (2 MB and more, out of place) whose tokens fill several 16 KB stages, the last of them
+    shorter (43 heads of 192 in bf16: 22 and 21; 128 of 576: nine of 13 and 11), beside tensors of one stage, with
+    padding: every row as the in-place form makes it, and some against the definition."""
+    g = torch.Generator(device=DEV).manual_seed(heads)
+    table, freq = api.li_rope_table(64), oracle.rope_frequencies(64)
+    pos = torch.randint(0, 200000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    pos[torch.tensor([0, 7, 8, 50, n - 1], device=DEV)] = -1
+    xs = [torch.randn(s, generator=g, device=DEV).to(dtype) for s in [(n, heads, dim), (n, 128), (n, 3, dim)]]
+    assert sum(x.numel() * x.element_size() for x in xs) >= 2 << 20
+    offsets = [offset, 32, offset]
+    outs = [torch.full_like(x, 7.0) for x in xs]
+    got = api.li_rope(xs, pos, table, layout=layout, offset=offsets, mscale=1.5, out=outs)
+    assert api.li_get_last_error() == LI_OK
+    dead, some = pos < 0, np.r_[0:10, 48:52, n - 4:n]
+    for x, o, off in zip(xs, got, offsets):
+        assert (o[dead] == 7).all()
+        same = x.clone()
+        api.li_rope(same, pos, table, layout=layout, offset=off, mscale=1.5, out=same)
+        assert torch.equal(same[~dead], o[~dead])
+        _check_rope(o.cpu()[some], x.cpu()[some], pos.cpu().numpy()[some].tolist(), freq, layout, off, 1.5)
 
 
 @pytest.mark.parametrize("kind", ["kv4", "bf16"])
