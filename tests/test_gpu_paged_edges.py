@@ -1,13 +1,13 @@
-"""Paged-cache operators at edges: tensors that share a buffer, heads over several stages of a bulk copy,
-values that all rows have in common, NaN far below the maximum.  Definitions: oracle.paged."""
+"""Paged-cache operators at edges: tensors that share a buffer, heads over several stages of a bulk copy, two rows a warp
+into the 4-bit cache, values that all rows have in common, NaN far below the maximum.  Definitions: oracle.paged."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import paged as oracle
 from sparse_attention_lightning_score_b200 import api
-from sparse_attention_lightning_score_b200._lib import LI_OK
-from tests.test_gpu_paged import DEV, Case, _check_rope, _i32
+from sparse_attention_lightning_score_b200._lib import LI_ERR_BOUNDS, LI_OK
+from tests.test_gpu_paged import DEV, Case, _check_rope, _i32, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -58,6 +58,39 @@ def test_rope_heads_over_several_stages(dtype, layout, n, heads, dim, offset):
         api.li_rope(same, pos, table, layout=layout, offset=off, mscale=1.5, out=same)
         assert torch.equal(same[~dead], o[~dead])
         _check_rope(o.cpu()[some], x.cpu()[some], pos.cpu().numpy()[some].tolist(), freq, layout, off, 1.5)
+
+
+# --------------------------------------------------------------------------- the 4-bit cache
+@pytest.mark.parametrize("n", [16383, 16384, 16385, 20001])
+@pytest.mark.parametrize("stride", [576, 584, 577])
+def test_kv4_write_of_many_rows(n, stride):
+    """From 16384 rows on a warp takes two (where rows are 16-byte aligned): padding and bad slots in the first and in the
+    second row of a pair, an odd last row, ones that are none; byte for byte what calls of fewer rows leave."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    rows = torch.randn(n, stride, generator=g, device=DEV).to(torch.bfloat16)[:, :576]
+    page, pages = 64, n // 64 + 3
+    slots = torch.randperm(pages * page, generator=g, device=DEV)[:n]
+    for i, bad in [(10, -1), (21, -1), (30, pages * page), (41, 1 << 40), (52, -1), (53, pages * page), (n - 2, -1)]:
+        slots[i] = bad
+    if n % 2:
+        slots[n - 1] = pages * page - 1 if (slots != pages * page - 1).all() else slots[n - 1]
+    cache = torch.randint(0, 255, (pages, page, 416), dtype=torch.uint8, generator=g, device=DEV)
+    want = cache.clone()
+    good = ((slots >= 0) & (slots < pages * page)).nonzero()[:, 0]
+    for part in good.split(5000):
+        api.li_kv4_write(rows[part], slots[part], want)
+    assert api.li_get_last_error() == LI_OK
+    api.li_kv4_write(rows, slots, cache)
+    assert api.li_get_last_error() == LI_ERR_BOUNDS
+    assert torch.equal(cache, want)
+    some = torch.cat([good[:30], good[40:60], good[-9:]])
+    assert np.array_equal(_np(cache.view(-1, 416)[slots[some]]), oracle.kv4_pack(rows[some].cpu()))
+    back = api.li_kv4_read(cache, slots)
+    assert api.li_get_last_error() == LI_ERR_BOUNDS
+    keep = torch.zeros(n, dtype=torch.bool, device=DEV)
+    keep[good] = True
+    assert (back[~keep] == 0).all()
+    assert np.array_equal(back[some].cpu().double().numpy(), oracle.kv4_unpack(oracle.kv4_pack(rows[some].cpu())))
 
 
 @pytest.mark.parametrize("kind", ["kv4", "bf16"])
