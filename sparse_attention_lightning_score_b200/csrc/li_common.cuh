@@ -257,7 +257,21 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
     return d;
 }
 
-// The same for a K-major operand stored with the 64-byte swizzle: rows of 64
+// Shared-memory descriptor for an MN-major operand with the 128-byte swizzle:
+// each 128-byte row holds 64 consecutive M (or N) elements of one K index, 8
+// rows form a 1024-byte swizzle atom, atoms follow each other along K every
+// `sbo` bytes and blocks of 64 M elements every `lbo` bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
+    d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
+    d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
+    d |= uint64_t(1u) << 46;
+    d |= uint64_t(2u) << 61;
+    return d;
+}
+
+// As sw128_kmajor_desc, for a K-major operand stored with the 64-byte swizzle: rows of 64
 // bytes, 8-row (512-byte) swizzle atoms 512 bytes apart, layout type
 // SWIZZLE_64B (4).
 __device__ __forceinline__ uint64_t sw64_kmajor_desc(uint32_t smem_addr) {

@@ -173,19 +173,6 @@ __device__ __forceinline__ bool group_any(int bar, bool yes) {
     return r != 0;
 }
 
-// MN-major operand with the 128-byte swizzle: each 128-byte row holds 64
-// consecutive M (or N) elements of one K index; atoms of 8 rows follow each other
-// along K every `sbo` bytes, blocks of 64 M elements every `lbo` bytes.
-__device__ __forceinline__ uint64_t pa_mnmajor_desc(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
-    d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
-    d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
-    d |= uint64_t(1u) << 46;
-    d |= uint64_t(2u) << 61;
-    return d;
-}
-
 // Reduction of N values over the warp: lane l ends with v[0] reduced for index l % N (log2 N steps keep
 // the half selected by one lane bit, the others join lanes that hold the same index).
 template <bool MAX, int N>
@@ -426,8 +413,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         constexpr uint32_t IDESC_O = idesc_f32acc(128, NH, kFmtBF16) | (1u << 15) | (1u << 16);
         // start addresses are in units of 16 bytes in the low 14 bits and stay below 2^14: plain additions
         const uint64_t k_desc = sw128_kmajor_desc(smem_u32(ks)), q_desc = sw128_kmajor_desc(smem_u32(qs));
-        const uint64_t v_desc = pa_mnmajor_desc(smem_u32(ks), PA_CHUNK, 1024);
-        const uint64_t p_desc = pa_mnmajor_desc(smem_u32(ps), PA_CHUNK, 1024);
+        const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(ks), PA_CHUNK, 1024);
+        const uint64_t p_desc = sw128_mnmajor_desc(smem_u32(ps), PA_CHUNK, 1024);
         const bool one = elect_one();
         auto load_q = [&](const PaUnit& x) {
             if (one) {

@@ -87,20 +87,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Shared-memory descriptor for an MN-major operand with the 128-byte swizzle:
-// each 128-byte row holds 64 consecutive M (or N) elements of one K index, 8
-// rows form a 1024-byte swizzle atom, atoms follow each other along K every
-// `sbo` bytes and blocks of 64 M elements every `lbo` bytes.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
-    d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
-    d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
-    d |= uint64_t(1u) << 46;
-    d |= uint64_t(2u) << 61;
-    return d;
-}
-
 // Reduce-scatter of 64 values over the warp: afterwards lane l holds, in v[0]
 // and v[1], the reduction over all 32 lanes of heads 2l and 2l+1.  Each step
 // keeps the half of the array selected by one lane bit and adds the partner's
