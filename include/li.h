@@ -554,6 +554,11 @@ li_status li_rope(const li_rope_tensor* tensors, int n_tensors, int tokens, cons
  *     s = e4m3(min(absmax / 6, 448)),   code_i = e2m1(x_i / s)   (nearest, ties to even;
  * beyond 6 the largest code; all zero when s is zero).  The value held is code * s,
  * which bf16 holds exactly.  A block with a NaN gets a NaN scale: it reads as NaN.
+ * There is no factor above the scales, which suit rows of about unit size: a block whose
+ * absmax is at most 6 * 2^-10 reads as zeros, one below 6 * 2^-6 has a scale in steps of
+ * 2^-9 (three bits or fewer), one above 6 * 448 saturates.  Rows of another size are
+ * multiplied by a power of two f first; the attention over them takes scale / f, and its
+ * output is divided by f.
  *   rows   [n, 576] bf16, `row_stride` elements apart (>= 576)
  *   slots  [n] int64 (li_block_tables); < 0 is skipped, one outside the cache is
  *          skipped and reported as LI_ERR_BOUNDS.  Slots of a call must differ: of two

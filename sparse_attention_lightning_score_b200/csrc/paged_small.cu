@@ -533,8 +533,9 @@ __device__ __forceinline__ void kv4_block(const uint32_t (&w)[8], uint2& code, u
         float y[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            // x / s: one correction makes a quotient that fp32 can hold exact, so ties between two codes
-            // are seen as ties; the conversion saturates beyond 6.  An infinity stands for the largest float.
+            // x / s: the product with the reciprocal, then Markstein's correction by the exact residual (IBM J. Res.
+            // Dev. 34, 1990), which makes a quotient that fp32 can hold exact, so ties between two codes are seen
+            // as ties; the conversion saturates beyond 6.  An infinity stands for the largest float.
             float x = k & 1 ? bf_hi(w[4 * j + (k >> 1)]) : bf_lo(w[4 * j + (k >> 1)]);
             if (top >= 0x7f800000u) x = fminf(fmaxf(x, -3.3e38f), 3.3e38f);
             const float q = x * r;

@@ -7,7 +7,7 @@ import torch
 from oracle import paged as oracle
 from sparse_attention_lightning_score_b200 import api
 from sparse_attention_lightning_score_b200._lib import LI_ERR_BOUNDS, LI_OK
-from tests.test_gpu_paged import DEV, Case, _check_rope, _i32, _np
+from tests.test_gpu_paged import DEV, U, Case, _check_rope, _i32, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -91,6 +91,33 @@ def test_kv4_write_of_many_rows(n, stride):
     keep[good] = True
     assert (back[~keep] == 0).all()
     assert np.array_equal(back[some].cpu().double().numpy(), oracle.kv4_unpack(oracle.kv4_pack(rows[some].cpu())))
+
+
+def test_kv4_range_of_the_scales():
+    """Blocks around the least absmax that does not read as zeros, the least of a normal scale and the largest that does
+    not saturate; and the same rows times a power of two, which the attention's scale and output undo."""
+    tops = [6 * 2.0 ** -10, 6 * 2.0 ** -10 * (1 + 2.0 ** -7), 6 * 2.0 ** -6, 6 * 2.0 ** -6 * (1 - 2.0 ** -8), 2688.0, 2704.0,
+            1e30, 0.0]
+    x = torch.zeros(1, 576)
+    for b, top in enumerate(tops):
+        x[0, 16 * b:16 * b + 16] = torch.linspace(-1, 1, 16) * top
+    rows = x.to(torch.bfloat16)
+    cache = api.li_kv4_write(rows.to(DEV), torch.tensor([0], device=DEV), api.li_kv4_cache(1, 1))
+    raw = oracle.kv4_pack(rows)
+    assert np.array_equal(_np(cache).reshape(1, 416), raw)
+    assert raw[0, 256:264].tolist() == [0, 1, 0x08, 0x08, 0x7e, 0x7e, 0x7e, 0]
+    assert np.abs(oracle.kv4_unpack(raw))[0, 16 * 4:16 * 7].max() == 2688
+
+    g = torch.Generator().manual_seed(17)
+    small = (torch.randn(300, 576, generator=g) * 2.0 ** -12).to(torch.bfloat16)
+    q, f, scale = torch.randn(1, 64, 576, generator=g).to(torch.bfloat16), 2.0 ** 12, 300.0
+    held = api.li_kv4_write((small * f).to(DEV), torch.arange(300, device=DEV), api.li_kv4_cache(3, 100))
+    table = _i32([[0, 1, 2]])
+    got = api.li_window_attention(q.to(DEV), held, _i32([299]), scale / f, 300, block_table=table)
+    ref, mag, top = oracle.attention(q[0].double().numpy(), oracle.kv4_unpack(oracle.kv4_pack(small * f)) / f, scale)
+    d = 2.0 ** -23 * (600 * top + 64 + 300 / 16)     # (the bound of test_gpu_paged, and the sum's share of the weights)
+    err = np.abs((got / f)[0].cpu().double().numpy() - ref)
+    assert np.all(err <= 2 * U * mag + U * np.abs(ref) + 2 * d[:, None] * mag)
 
 
 @pytest.mark.parametrize("kind", ["kv4", "bf16"])
