@@ -879,6 +879,7 @@ static li_status paged_attention(const void* q, PagedAttnArgs a, const li_attn_d
     if (!a.table && (int64_t)d.requests * d.max_blocks > d.num_pages) return LI_ERR_INVALID_ARG;
     if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return LI_ERR_INVALID_ARG;
     if ((!a.cache && d.num_pages > 0) || !aligned(a.cache, 16)) return LI_ERR_INVALID_ARG;
+    if (!aligned(a.table, 4) || !aligned(a.req, 4) || !aligned(a.sel, 4) || !aligned(a.pos, 4)) return LI_ERR_INVALID_ARG;
     a.rows = d.rows;
     a.heads = d.heads;
     a.requests = d.requests;
