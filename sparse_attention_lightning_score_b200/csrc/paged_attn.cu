@@ -42,8 +42,8 @@
 // of a pair (540 to 700 cycles to expand, about 1000 to gather) are hidden only
 // under the value products of the pairs behind it.  Measured: 2.8 us a tile of 64
 // heads in 4 bits with few CTAs, 3.5 with all SMs busy (128 heads over a window of
-// 131071: 68 us, 0.54 PFLOP/s); bf16 2.7 and 3.4 (1024 tokens x 128 heads, window
-// 512: 280 us, 0.54 PFLOP/s).
+// 131071: 67 us, 0.54 PFLOP/s); bf16 2.7 and 3.4 (1024 tokens x 128 heads, window
+// 512: 281 us, 0.54 PFLOP/s).
 // With few units the visible tiles are split over several CTAs; a second kernel
 // merges the parts (see paged_attn_plan for the rule).
 #include <cuda_fp16.h>
@@ -825,8 +825,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 // largest m_s (maxima are in the log2 domain).  A CTA takes 512 / ST latent elements of one (head, token), four
 // to a thread, the parts dealt over its ST stripes of threads, eight in flight in each; the weights are made once in
 // shared memory.  Latency bound: an L2 read of the maxima, then the parts.  ST = 1 keeps the CTAs few (a whole call
-// of 24 tokens x 128 heads in 3 parts: 25.4 us, 32.1 with ST = 4; 8 x 128 in 8: 21.8 and 22.6), ST = 4 shortens the walk
-// over more than eight parts (1 x 64 in 16 parts: 12.2 us, 13.2 with ST = 1; 1 x 128 in 74: 66.7 and 82.2).
+// of 24 tokens x 128 heads over 2048 rows in 3 parts: 36.5 us, 43.0 with ST = 4; 8 x 128 in 8: 20.0 and 22.0), ST = 4
+// shortens the walk over more than eight parts (1 x 64 in 16 parts: 11.5 us, 11.9 with ST = 1; 1 x 128 over 131071 in
+// 74: 63.5 and 68.7).
 constexpr int PA_MERGE = 128;
 constexpr float PA_UNWRITTEN = -1.f;  // weight of a part without a visible position: it has not been written
 template <int ST>
@@ -927,10 +928,14 @@ li_status launch_units(const CUtensorMap& qmap, const CUtensorMap& kmap, const P
 // its heads (the end writes them); parts cost a merge, and their fp32 sums are written and read once more.  For
 // each number of waves the largest count of splits that fits is tried, lowered as far as the longest share stays
 // the same.  The constants are fitted to whole calls; a further tile alone takes 2.8 / 2.2 / 2.0 us at 64 / 32 / 16
-// heads a unit with 4-bit rows (bf16: 2.7 / 2.2 / 2.1).  What the rule decides between, as measured: 1 token x 64 heads,
-// 2048 rows: 16 heads in 16 splits 11.5, 64 heads in 16 splits 14.5; 8 x 128, 2048 rows: 64 in 8 22.3, 32 in 4 23.3, 16
-// in 2 31.9; 32 x 128, 516 rows: 32 unsplit 20.4, 64 in 2 24.8, 64 unsplit 24.9; 74 x 16, 1000 rows: 16 in 2 20.9,
-// unsplit 27.0; 1 x 128, 131071 rows: 64 in 74 68, 32 in 74 98, 64 in 148 84.
+// heads a unit with 4-bit rows (bf16: 2.7 / 2.2 / 2.1), near enough for one set to choose well for both.  What the rule
+// decides between, as measured in a graph (4 bits; bf16), its choice first: 1 token x 64 heads, 2048 rows: 16 heads in 16
+// splits 11.3; 10.8, 64 heads in 16 14.6; 13.2.  8 x 128, 2048 rows: 64 in 8 19.8; 18.0, 32 in 4 21.8; 21.2, 16 in 2 30.5;
+// 29.9.  32 x 128, 516 rows: 32 unsplit 20.4; 19.7, 64 in 2 25.1; 23.3, 64 unsplit 25.0; 23.0.  32 x 128, 2048 rows: 64 in 2
+// 44.3; 45.4, 32 unsplit 51.5; 54.5.  74 x 16, 1000 rows: 16 in 2 20.2; 21.4, unsplit 27.6; 29.5.  1 x 128, 131071 rows: 64
+// in 74 63.8; 69.3, 32 in 37 88.8; 97.5, 64 in 148 75.3; 80.3.  (4 x 128, 2048 rows: its 64 in 16 takes 16.0; 14.7, 32 in 8
+// 15.5; 15.0.)  The rule knows the longest list alone: a batch of one long list and many short ones is split for the long
+// one, whose units then share few SMs (32 x 128, one of 131071 and 31 of 1000 positions: 447 us, most of it on 18 SMs).
 PagedAttnPlan paged_attn_plan(int rows, int heads, int positions, int sms) {
     const int tiles = (positions + PA_M - 1) / PA_M;
     static const struct {
