@@ -482,6 +482,7 @@ li_status li_sparse_attention(const void* q_bf16, const void* kv_bf16, int64_t c
  *   positions  [max_tokens] int32 (out): its position in the request
  *   requests_of [max_tokens] int32 (out): its request
  *   starts     [requests + 1] int32 (out): first token of each request, then the total
+ *              (2^31 - 1 where it would be more)
  *   free_next  [1] int32 (out): the first entry of free_pages not taken; may not
  *              be free_start itself (pass the two buffers in turn)
  * Entries of the three token arrays after the last token are -1, which the calls

@@ -575,7 +575,7 @@ def li_kv4_cache(num_pages: int, page_size: int, device="cuda") -> torch.Tensor:
 
 
 def li_kv4_write(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, stream=None):
-    """rows bf16 [n, 576] (any row stride) quantised to 4 bits and written to `slots` int64 [n] (negative:
+    """rows bf16 [n, 576] (a row stride of 576 or more) quantised to 4 bits and written to `slots` int64 [n] (negative:
     skipped; no slot twice) of cache uint8 [pages, page_size, 416].  Returns cache."""
     if stream is not None:
         with _under(stream, rows):
